@@ -60,6 +60,7 @@
 #include <mutex>
 #include <vector>
 
+#include "grouped_tiles.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -75,7 +76,6 @@ constexpr int NUM_EPI_WARPS = 8;              // two per TMEM lane quadrant, eac
 constexpr int NUM_THREADS = 64 + 32 * NUM_EPI_WARPS;  // producer warp, MMA warp, epilogue warps
 constexpr uint32_t TMEM_COLS = 512;             // two BN-column fp32 accumulators
 constexpr int CTRL_BYTES = 512;  // mbarriers (bytes 0..255) and flags (256..)
-constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s: far beyond any legitimate wait
 
 // Per-CTA pipeline geometry.  PAIR = 1: one CTA computes a 128 x 256 tile and
 // loads all four 64-column B boxes (48 KB a stage, 4 stages).  PAIR = 2: a
@@ -128,38 +128,6 @@ struct GemmParams {
   int a_direct;  // gate_up: A rows are rows within the expert's segment (A = x)
   int k;         // routed slots per token (a slot's token is slot / k)
 };
-
-struct TileCoord {
-  int e, row0, rows, n, piece;  // piece: global index of the 128-row piece
-};
-
-// Tile t -> (expert, first permuted row of the tile, valid rows, output
-// column block).  s_mt is the exclusive prefix of per-expert pieces of
-// `piece` rows (s_mt[E] = total).
-__device__ __forceinline__ TileCoord decode_tile(int t, int n_tiles, int E, const int* s_mt, const int* s_off,
-                                                 int piece) {
-  int lo = 0, hi = E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s_mt[mid] * n_tiles <= t) lo = mid;
-    else hi = mid;
-  }
-  TileCoord c;
-  c.e = lo;
-  const int local = t - s_mt[lo] * n_tiles;
-  const int mt = s_mt[lo + 1] - s_mt[lo];
-  c.n = local / mt;
-  const int m = local - c.n * mt;
-  c.row0 = s_off[lo] + m * piece;
-  c.rows = min(piece, s_off[lo + 1] - c.row0);
-  c.piece = s_mt[lo] + m;
-  return c;
-}
-
-__device__ __forceinline__ bool wait_time_only(uint32_t bar, uint32_t parity) {
-  int never = 0;
-  return mbar_wait(bar, parity, &never, kTimeoutNs);
-}
 
 // ------------------------------------------ single-launch cross-CTA hand-off
 // A gate_up tile's epilogue warps each publish their h stores with one
@@ -232,10 +200,6 @@ __device__ __forceinline__ bool wait_arrivals(const int* counter, int target, vo
 // memory (row stride 80 B: conflict-free), then stores 8 rows x 64 B per
 // instruction, so each store fills whole 32-byte sectors of contiguous
 // columns instead of scattering 16-byte pieces over 32 rows.
-constexpr int kStageRowBytes = 80;
-constexpr int kStageWarpBytes = 32 * kStageRowBytes;  // 2560 B per epilogue warp
-constexpr int kOutChunk = 32;                          // output columns per chunk
-
 // gate_up: 32 h columns starting at tile h column hc (relative to the tile),
 // whose accumulator columns start at TMEM column tcol: concatenated, gate
 // of h column hc + i at tcol + i and up at tcol + up_off + i; interleaved,
@@ -963,6 +927,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 // same shapes, call after call).
 struct MapKey {
   const void* base;
+  CUtensorMapDataType type;
   int rank;
   cuuint64_t dims[5];
   cuuint64_t strides[4];
@@ -970,7 +935,7 @@ struct MapKey {
 };
 
 bool same_key(const MapKey& a, const MapKey& b) {
-  if (a.base != b.base || a.rank != b.rank) return false;
+  if (a.base != b.base || a.type != b.type || a.rank != b.rank) return false;
   for (int i = 0; i < a.rank; ++i)
     if (a.dims[i] != b.dims[i] || a.box[i] != b.box[i]) return false;
   for (int i = 0; i + 1 < a.rank; ++i)
@@ -987,10 +952,13 @@ struct MapCache {
 };
 thread_local MapCache t_maps;
 
-bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
-                     const cuuint64_t* strides_bytes, const cuuint32_t* box) {
+}  // namespace
+
+bool encode_tiled_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+                      const cuuint64_t* strides_bytes, const cuuint32_t* box) {
   MapKey key = {};
   key.base = base;
+  key.type = type;
   key.rank = rank;
   for (int i = 0; i < rank; ++i) {
     key.dims[i] = dims[i];
@@ -1007,7 +975,7 @@ bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint6
   auto enc = encoder();
   if (enc == nullptr) return false;
   const cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base),
+  const CUresult r = enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base),
                          dims, strides_bytes, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1022,6 +990,13 @@ bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint6
   c.key[slot] = key;
   c.map[slot] = *map;
   return true;
+}
+
+namespace {
+
+bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                     const cuuint64_t* strides_bytes, const cuuint32_t* box) {
+  return encode_tiled_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides_bytes, box);
 }
 
 template <int PAIR>

@@ -170,11 +170,79 @@ int mega_ffn_counters(int R, int E);
 cudaError_t launch_mega_ffn(const GroupedGemmArgs& up, const GroupedGemmArgs& down, int* arrivals,
                             cudaStream_t stream);
 
+// Encodes (or takes from a small per-thread cache) a 128-byte-swizzled tensor
+// map of `rank` dimensions; strides in bytes, from the second dimension on.
+bool encode_tiled_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+                      const cuuint64_t* strides_bytes, const cuuint32_t* box);
+
 // Resolves cuTensorMapEncodeTiled through the runtime (no libcuda link).
 bool tensor_map_encoder_available();
 
 // Whether the gate_up GEMM gathers its rows of x itself in this process
 // (MOE_B200_FUSED_GATHER=1 with single-CTA tiles; off by default).
 bool fused_gather_enabled();
+
+// ------------------------------------ tokens sorted by expert and back
+// Rows are `vec` 16-byte vectors.  spread: rows_out[p] = w * tok_in[t]; gather:
+// tok_out[t] = sum_j w * rows_in[p]; with d_weights (may be null) also
+// d_weights[t*k+j] = <tok_in[t], rows_in[p]>.  p = inverse[t*k+j].
+struct RowsArgs {
+  const void* tok_in;
+  void* tok_out;
+  const void* rows_in;
+  void* rows_out;
+  const int32_t* inverse;  // [R]
+  const float* weights;    // [R] or null for 1
+  float* d_weights;        // [R] or null
+  int T, k, R, vec;
+};
+cudaError_t launch_rows_spread(const RowsArgs& a, bool f32, cudaStream_t stream);
+cudaError_t launch_rows_gather(const RowsArgs& a, bool f32, cudaStream_t stream);
+
+// ------------------------------------------------------ router gradient
+constexpr int kGradMaxBlocks = 1024;
+struct RouterGradArgs {
+  const void* logits;
+  int64_t stride;            // of logits and d_logits
+  int T, E, k, S;
+  float route_scale;
+  const float* global_scale; // device [1] or null
+  const int32_t* idx;        // [T,k]
+  const float* d_weights;    // [T,k]
+  const float* d_sink;       // [T,S] or null for zero
+  void* d_logits;            // [T,stride], columns 0 .. E+S-1 written
+  double* partial;           // [kGradMaxBlocks] or null: no d_global_scale
+};
+cudaError_t launch_route_grad(const RouterGradArgs& a, bool sink, bool bf16, float* d_global_scale,
+                              cudaStream_t stream);
+
+// ------------------------------------------------------------ 8-bit experts
+// Bytes of a row of n 8-bit values: TMA row strides are multiples of 16.
+inline int int8_pitch(int n) { return (n + 15) / 16 * 16; }
+// q[p] = the row quantised by its largest magnitude, scales[p] = that / 127,
+// for the k positions p of every row (inverse, may be null: p = the row).
+// total (may be null): device int, rows from it on are left alone.
+cudaError_t launch_quantize_rows(const __nv_bfloat16* in, int rows, int n, const int32_t* inverse, int k, int R,
+                                 const int32_t* total, int8_t* q, float* scales, cudaStream_t stream);
+// W [E,K,N] bf16 -> q [E,N,int8_pitch(K)], scales [E,N] (per column).
+cudaError_t launch_quantize_weights(const __nv_bfloat16* w, int E, int K, int N, int8_t* q, float* scales,
+                                    cudaStream_t stream);
+struct Int8GemmArgs {
+  const int32_t* offsets;    // [E+1]
+  int E, R, H, D;
+  int down;                  // 0: gate_up with the activation, 1: down
+  int gate_up_format;
+  int activation;
+  float alpha, limit;
+  const int8_t* A;           // [R, int8_pitch(K)]
+  const float* a_scales;     // [R]
+  const int8_t* W;           // [E, N, int8_pitch(K)]
+  const float* w_scales;     // [E, N]
+  const __nv_bfloat16* bias; // [E, N] or null
+  __nv_bfloat16* out;        // [R, D] or [R, H], in sorted order
+  int* status;
+  int num_sms;
+};
+cudaError_t launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream);
 
 }  // namespace moe

@@ -5,9 +5,7 @@
 #include <cstring>
 #include <mutex>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "kernels.cuh"
+#include "api_common.cuh"
 
 using moe::kMaxExperts;
 using moe::kMaxTopK;
@@ -24,8 +22,10 @@ struct DeviceInfo {
 DeviceInfo g_devices[kMaxDevices];
 std::mutex g_devices_mu;
 
-// The current device must be compute capability 10.0 (the library's code is
-// sm_100a only) and the driver must expose the tensor-map encoder.
+}  // namespace
+
+namespace moe {
+
 moe_status_t current_device(int* num_sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
@@ -46,8 +46,6 @@ moe_status_t current_device(int* num_sms) {
   *num_sms = d.num_sms;
   return MOE_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 moe_status_t validate_config(const moe_config_t* c) {
   if (c == nullptr) return MOE_ERR_INVALID_ARGUMENT;
@@ -87,7 +85,25 @@ moe_status_t validate_config(const moe_config_t* c) {
   return MOE_OK;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+bool nvtx_enabled() {
+  static const bool on = [] {
+    const char* env = std::getenv("MOE_B200_NVTX");
+    return env != nullptr && env[0] == '1';
+  }();
+  return on;
+}
+
+}  // namespace moe
+
+using moe::align256;
+using moe::aligned16;
+using moe::at;
+using moe::cuda_status;
+using moe::current_device;
+using moe::NvtxRange;
+using moe::validate_config;
+
+namespace {
 
 // The extensions of moe_forward_ex (token mask, router weight before the
 // experts, shared experts), already validated.
@@ -160,11 +176,6 @@ WsLayout ws_layout(const moe_config_t* c, const Extras* ex = nullptr) {
   return L;
 }
 
-template <typename T>
-T* at(void* base, size_t off) {
-  return reinterpret_cast<T*>(static_cast<char*>(base) + off);
-}
-
 moe_status_t check_workspace(const moe_config_t* c, const void* ws, size_t bytes, WsLayout* L,
                              const Extras* ex = nullptr) {
   *L = ws_layout(c, ex);
@@ -177,8 +188,6 @@ moe_status_t check_bias(const moe_config_t* c, const void* gate_up_b, const void
   if (c->has_bias) return (gate_up_b != nullptr && down_b != nullptr) ? MOE_OK : MOE_ERR_INVALID_ARGUMENT;
   return (gate_up_b == nullptr && down_b == nullptr) ? MOE_OK : MOE_ERR_INVALID_ARGUMENT;
 }
-
-moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 moe::RouterArgs router_args(const moe_config_t* c, const void* logits, const float* bias, const float* gscale,
                             int32_t* idx, float* w, float* sink_w, int* status_reset) {
@@ -202,29 +211,6 @@ moe::RouterArgs router_args(const moe_config_t* c, const void* logits, const flo
 }
 
 // Records ev[i] on the stream when events are requested.
-// NVTX ranges (MOE_B200_NVTX=1): one per API call and one around the
-// enqueue of each kernel, named "moe.<stage>", for a timeline profiler to
-// line up with the kernels.  Off by default (no NVTX call is made).
-bool nvtx_enabled() {
-  static const bool on = [] {
-    const char* env = std::getenv("MOE_B200_NVTX");
-    return env != nullptr && env[0] == '1';
-  }();
-  return on;
-}
-
-struct NvtxRange {
-  const bool on;
-  explicit NvtxRange(const char* name) : on(nvtx_enabled()) {
-    if (on) nvtxRangePushA(name);
-  }
-  ~NvtxRange() {
-    if (on) nvtxRangePop();
-  }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
 struct Recorder {
   cudaEvent_t const* ev;
   cudaStream_t stream;
