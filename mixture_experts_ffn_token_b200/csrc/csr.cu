@@ -170,6 +170,8 @@ __global__ void __launch_bounds__(kCsrThreads) csr_scatter_kernel(const int32_t*
       perm[pos] = static_cast<int32_t>(s);
       if (inv != nullptr) inv[s] = pos;
       if ((peers & lt_mask) == 0) my[e] += __popc(peers);
+    } else if (inv != nullptr && s < R) {
+      inv[s] = -1;  // the slot went to no expert
     }
     __syncwarp();
   }
@@ -326,6 +328,8 @@ __global__ void __launch_bounds__(kCsrThreads) csr_fused_kernel(const int32_t* _
       perm[pos] = static_cast<int32_t>(s);
       if (inv != nullptr) inv[s] = pos;
       if ((peers & lt_mask) == 0) my[e] += __popc(peers);
+    } else if (inv != nullptr && s < R) {
+      inv[s] = -1;  // the slot went to no expert
     }
     __syncwarp();
   }
