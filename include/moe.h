@@ -153,7 +153,8 @@ moe_status_t moe_route(const moe_config_t* cfg, const void* logits, const float*
  *   expert_offsets [E+1] int32 out: exclusive prefix sum of per-expert counts.
  *   permutation    [R] int32 out: slot ids sorted by expert, ascending slot
  *                  within one expert (stable; token of slot s is s / k).
- *   inverse        [R] int32 out or NULL: position of slot s in permutation.
+ *   inverse        [R] int32 out or NULL: position of slot s in permutation,
+ *                  -1 for a slot that was skipped.
  * The result is deterministic (no atomics decide any order). */
 moe_status_t moe_create_indices(const moe_config_t* cfg, const int32_t* expert_indices,
                                 int32_t* expert_offsets, int32_t* permutation, int32_t* inverse,
@@ -319,6 +320,127 @@ moe_status_t moe_forward_ex(const moe_config_t* cfg, const moe_extras_t* extras,
 moe_status_t moe_create_indices_noalloc(const moe_config_t* cfg, const int32_t* expert_indices,
                                         int32_t* expert_offsets, int32_t* permutation, int32_t* inverse,
                                         moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Tokens sorted by expert and back, and the gradients.
+ *
+ * With w_s the routing weight of slot s = t*k + j and p = inverse[s] its
+ * position among the rows sorted by expert (moe_create_indices), a slot whose
+ * p lies outside [0, R) went to no expert and takes part in nothing:
+ *   moe_dispatch           rows[p] = w_s * x[t]
+ *   moe_dispatch_backward  d_x[t]  = sum_j w_s * d_rows[p];  d_w_s = <x[t], d_rows[p]>
+ *   moe_combine            out[t]  = sum_j w_s * rows[p]
+ *   moe_combine_backward   d_rows[p] = w_s * d_out[t];       d_w_s = <d_out[t], rows[p]>
+ * Arguments:
+ *   dtype              MOE_DTYPE_BF16 or MOE_DTYPE_F32, of every row tensor.
+ *   x, out, d_x, d_out [T, H]; rows, d_rows [R, H] in sorted order.  16-byte
+ *                      aligned, and no output overlaps an input.
+ *   inverse            [R] int32, each position named by one slot at most.
+ *   expert_weights     [T, k] fp32 in slot order, or NULL for 1.
+ *   d_expert_weights   [T, k] fp32 out or NULL; it needs the forward pass's
+ *                      x (moe_dispatch_backward) or rows
+ *                      (moe_combine_backward), which are not read otherwise
+ *                      and may then be NULL.  0 for a slot of no expert.
+ * [T, H] and [T, k] outputs are fully overwritten; rows of no slot (those
+ * behind the last expert's segment) are left as they were.
+ * Numerics: products and sums in fp32, j ascending, each output rounded once;
+ * the inner products in fp32 in a fixed order, so results are the same bits
+ * on every run.  One launch each, no workspace. */
+moe_status_t moe_dispatch(const moe_config_t* cfg, moe_dtype_t dtype, const void* x, const int32_t* inverse,
+                          const float* expert_weights, void* rows, moe_stream_t stream);
+moe_status_t moe_dispatch_backward(const moe_config_t* cfg, moe_dtype_t dtype, const void* d_rows, const void* x,
+                                   const int32_t* inverse, const float* expert_weights, void* d_x,
+                                   float* d_expert_weights, moe_stream_t stream);
+moe_status_t moe_combine(const moe_config_t* cfg, moe_dtype_t dtype, const void* rows, const int32_t* inverse,
+                         const float* expert_weights, void* out, moe_stream_t stream);
+moe_status_t moe_combine_backward(const moe_config_t* cfg, moe_dtype_t dtype, const void* d_out, const void* rows,
+                                  const int32_t* inverse, const float* expert_weights, void* d_rows,
+                                  float* d_expert_weights, moe_stream_t stream);
+
+/* Bytes of device workspace that moe_route_backward (with d_global_scale) and
+ * moe_grouped_linear_int8 need.  Host only.  A moe_workspace_size() workspace
+ * is not required for them; calls that may overlap on the GPU, replays of two
+ * captured graphs among them, need a workspace each. */
+moe_status_t moe_operator_workspace_size(const moe_config_t* cfg, size_t* bytes);
+
+/* The gradient of moe_route's weights with respect to its logits, for the
+ * selection that moe_route made (which has no gradient, nor has expert_bias):
+ *   softmax  w = softmax(z_selected):   d_z_i = w_i sum_j w_j (d_w_i - d_w_j)
+ *   sink     p = softmax(log sigmoid z) over selected and sink lanes, w = c p,
+ *            c = route_scale * global_scale:
+ *            d_z_i = c p_i sigmoid(-z_i) sum_j p_j (d_w_i - d_w_j)
+ *            d_global_scale = route_scale * sum over all tokens of p_i d_w_i
+ *   logits            as moe_route's.
+ *   global_scale      as moe_route's (NULL = 1); NULL for SOFTMAX_TOPK.
+ *   expert_indices    [T, k] as moe_route returned them; an entry outside
+ *                     [0, E) takes part in nothing, an expert named twice gets
+ *                     the sum of both.
+ *   d_expert_weights  [T, k] fp32.
+ *   d_sink_weights    [T, S] fp32 or NULL for zero; NULL when S = 0.
+ *   d_logits          [T, logits_row_stride] of logits_dtype out: columns
+ *                     0 .. E+S-1 overwritten (zero where nothing was
+ *                     selected), the tail of a wider row left as it was.
+ *   d_global_scale    [1] fp32 out or NULL; SIGMOID_SINK only.
+ *   workspace         moe_operator_workspace_size(), only with d_global_scale
+ *                     (else it may be NULL).
+ * Numerics: fp32, the sum of d_global_scale in fp64; deterministic. */
+moe_status_t moe_route_backward(const moe_config_t* cfg, const void* logits, const float* global_scale,
+                                const int32_t* expert_indices, const float* d_expert_weights,
+                                const float* d_sink_weights, void* d_logits, float* d_global_scale, void* workspace,
+                                size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' products in 8-bit integers, with a scale for each token row
+ * and each weight column.  A value a of a row (or column) whose largest
+ * magnitude is m is held as q = rint(127 a / m), ties to even, with the scale
+ * m / 127; a row or column that holds an infinity or a NaN gets a NaN scale,
+ * one of zeros a scale of 0.  8-bit rows of n values are MOE_INT8_PITCH(n)
+ * bytes apart (the padding is written as zero and never read).
+ * As used together:  moe_dispatch_int8 -> moe_grouped_linear_int8(GATE_UP) ->
+ * moe_quantize_rows -> moe_grouped_linear_int8(DOWN) -> moe_combine. */
+#define MOE_INT8_PITCH(n) (((n) + 15) / 16 * 16)
+#define MOE_INT8_MAX_K 131072 /* 127 * 127 * K stays in 32 bits; a longer K is MOE_ERR_UNSUPPORTED */
+
+/* The two contractions: GATE_UP has K = H and N = 2D columns in the layout of
+ * cfg->gate_up_format, DOWN has K = D and N = H. */
+typedef enum { MOE_GATE_UP = 0, MOE_DOWN = 1 } moe_contraction_t;
+
+/* moe_dispatch of x [T, H] bf16 to 8-bit rows: every token is quantised once
+ * and written to its slots' positions.
+ *   rows_q      [R, MOE_INT8_PITCH(H)] out, row_scales [R] fp32 out; rows of
+ *               no slot are left as they were. */
+moe_status_t moe_dispatch_int8(const moe_config_t* cfg, const void* x, const int32_t* inverse, int8_t* rows_q,
+                               float* row_scales, moe_stream_t stream);
+
+/* The activations h [R, D] bf16 to 8-bit rows, in place in the sorted order.
+ *   expert_offsets  [E+1] or NULL: with it, only the rows before
+ *                   expert_offsets[E] are read and written.
+ *   rows_q          [R, MOE_INT8_PITCH(D)] out, row_scales [R] fp32 out. */
+moe_status_t moe_quantize_rows(const moe_config_t* cfg, const void* h, const int32_t* expert_offsets, int8_t* rows_q,
+                               float* row_scales, moe_stream_t stream);
+
+/* The weights of one contraction, once, when they are loaded: w [E, K, N] bf16
+ * (gate_up_proj or down_proj as moe_forward takes them) to 8-bit rows of K.
+ *   w_q       [E, N, MOE_INT8_PITCH(K)] out, w_scales [E, N] fp32 out. */
+moe_status_t moe_quantize_weights(const moe_config_t* cfg, moe_contraction_t which, const void* w, int8_t* w_q,
+                                  float* w_scales, moe_stream_t stream);
+
+/* One contraction over rows sorted by expert, on the tensor cores:
+ *   y[p, n] = (sum_k rows_q[p, k] * w_q[e, n, k]) * row_scales[p] * w_scales[e, n] + bias[e, n]
+ * for p in [expert_offsets[e], expert_offsets[e+1]); GATE_UP stores
+ * h = activation(gate, up) [R, D], DOWN stores y [R, H].
+ *   rows_q, w_q, w_scales, out, bias  16-byte aligned.
+ *   bias       [E, N] bf16, per has_bias.
+ *   out        bf16, rows at and behind expert_offsets[E] left as they were.
+ *   workspace  moe_operator_workspace_size(); its status word is reset by the
+ *              call and read with moe_device_status (MOE_DEVICE_ERR_CSR: the
+ *              offsets are no CSR of at most R rows, nothing was written).
+ * Numerics: exact 32-bit integer sums, scales, bias and activation in fp32,
+ * one rounding to bf16; deterministic. */
+moe_status_t moe_grouped_linear_int8(const moe_config_t* cfg, moe_contraction_t which, const int8_t* rows_q,
+                                     const float* row_scales, const int8_t* w_q, const float* w_scales,
+                                     const void* bias, const int32_t* expert_offsets, void* out, void* workspace,
+                                     size_t workspace_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

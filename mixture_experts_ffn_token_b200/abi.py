@@ -24,6 +24,7 @@ ROUTERS = {"softmax_topk": 0, "sigmoid_sink": 1}
 FORMATS = {"concatenated": 0, "interleaved": 1}
 ACTIVATIONS = {"silu": 0, "swigluoai": 1, "gelu_tanh": 2}
 DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+CONTRACTIONS = {"gate_up": 0, "down": 1}
 DEVICE_ERR_EXPERT_INDEX = 0x1
 DEVICE_ERR_CSR = 0x2
 DEVICE_ERR_TIMEOUT_GEMM1 = 0x4
@@ -35,7 +36,9 @@ STAGE_NAMES = ("router", "csr_count", "csr_scan", "csr_scatter", "gather", "gemm
 
 EXPORTED = ("moe_status_string", "moe_workspace_size", "moe_route", "moe_create_indices", "moe_grouped_ffn",
             "moe_forward", "moe_forward_timed", "moe_device_status", "moe_create_indices_noalloc",
-            "moe_workspace_size_ex", "moe_forward_ex", "moe_single_launch_ffn")
+            "moe_workspace_size_ex", "moe_forward_ex", "moe_single_launch_ffn", "moe_operator_workspace_size",
+            "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward", "moe_route_backward",
+            "moe_dispatch_int8", "moe_quantize_rows", "moe_quantize_weights", "moe_grouped_linear_int8")
 NUM_STAGE_EVENTS_EX = 13
 STAGE_NAMES_EX = ("router", "csr_count", "csr_scan", "csr_scatter", "gather", "gemm_gate_up", "gemm_down",
                   "shared_index", "shared_gather", "shared_gemm_gate_up", "shared_gemm_down", "combine")
@@ -135,6 +138,19 @@ def load_library():
     lib.moe_forward_ex.argtypes = [cfgp, exp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
     lib.moe_single_launch_ffn.restype = ctypes.c_int
     lib.moe_single_launch_ffn.argtypes = [ctypes.POINTER(ctypes.c_int32)]
+    ci = ctypes.c_int
+    lib.moe_operator_workspace_size.argtypes = [cfgp, ctypes.POINTER(ctypes.c_size_t)]
+    lib.moe_dispatch.argtypes = [cfgp, ci, vp, vp, vp, vp, vp]
+    lib.moe_dispatch_backward.argtypes = [cfgp, ci, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_combine.argtypes = [cfgp, ci, vp, vp, vp, vp, vp]
+    lib.moe_combine_backward.argtypes = [cfgp, ci, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_route_backward.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_dispatch_int8.argtypes = [cfgp, vp, vp, vp, vp, vp]
+    lib.moe_quantize_rows.argtypes = [cfgp, vp, vp, vp, vp, vp]
+    lib.moe_quantize_weights.argtypes = [cfgp, ci, vp, vp, vp, vp]
+    lib.moe_grouped_linear_int8.argtypes = [cfgp, ci, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    for name in EXPORTED[EXPORTED.index("moe_operator_workspace_size"):]:
+        getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -337,3 +353,184 @@ def moe_device_status(workspace, stream=None) -> int:
     if st not in (MOE_OK, MOE_ERR_DEVICE_TIMEOUT):
         raise MoEError(st, "moe_device_status")
     return v.value
+
+
+# ---------------------------------------------------------------------------
+# Tokens sorted by expert and back with their gradients, the router's
+# gradient, and the experts' products in 8-bit integers.  These check their
+# tensors (type, size, dense layout, the current device) before the call: a
+# ValueError means that nothing was enqueued.
+
+def _take(device, name, t, dtype, numel, required=True):
+    """The data pointer of a dense tensor of `numel` elements on the current device."""
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current CUDA device ({device}), not on {t.device}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements, not {t.numel()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be dense (contiguous)")
+    return t.data_ptr()
+
+
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
+def _rows_dtype(name, t):
+    code = None if t is None else DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be a bfloat16 or float32 tensor")
+    return code
+
+
+def int8_pitch(n: int) -> int:
+    """Bytes between 8-bit rows of n values (MOE_INT8_PITCH)."""
+    return (n + 15) // 16 * 16
+
+
+def moe_operator_workspace_size(cfg: MoEConfig) -> int:
+    """Bytes of workspace of moe_route_backward and moe_grouped_linear_int8."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_operator_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_operator_workspace_size")
+    return n.value
+
+
+def moe_dispatch(cfg, x, inverse, rows, expert_weights=None, stream=None):
+    """rows[inverse[t*k+j]] = expert_weights[t, j] * x[t]: tokens [T, H] (bf16
+    or fp32) to rows sorted by expert [T*k, H]."""
+    dt, dev = _rows_dtype("x", x), _device()
+    T, H, R = cfg.num_tokens, cfg.hidden_dim, cfg.num_tokens * cfg.top_k
+    _check(load_library().moe_dispatch(
+        ctypes.byref(cfg), dt, _take(dev, "x", x, x.dtype, T * H), _take(dev, "inverse", inverse, torch.int32, R),
+        _take(dev, "expert_weights", expert_weights, torch.float32, R, False),
+        _take(dev, "rows", rows, x.dtype, R * H), _stream(stream)), "moe_dispatch")
+
+
+def moe_dispatch_backward(cfg, d_rows, inverse, d_x, x=None, expert_weights=None, d_expert_weights=None, stream=None):
+    """d_x[t] = sum_j expert_weights[t, j] * d_rows[inverse[t*k+j]] and, given x,
+    d_expert_weights[t, j] = <x[t], d_rows[inverse[t*k+j]]>."""
+    dt, dev = _rows_dtype("d_rows", d_rows), _device()
+    T, H, R = cfg.num_tokens, cfg.hidden_dim, cfg.num_tokens * cfg.top_k
+    _check(load_library().moe_dispatch_backward(
+        ctypes.byref(cfg), dt, _take(dev, "d_rows", d_rows, d_rows.dtype, R * H),
+        _take(dev, "x", x, d_rows.dtype, T * H, d_expert_weights is not None),
+        _take(dev, "inverse", inverse, torch.int32, R),
+        _take(dev, "expert_weights", expert_weights, torch.float32, R, False),
+        _take(dev, "d_x", d_x, d_rows.dtype, T * H),
+        _take(dev, "d_expert_weights", d_expert_weights, torch.float32, R, False), _stream(stream)),
+        "moe_dispatch_backward")
+
+
+def moe_combine(cfg, rows, inverse, out, expert_weights=None, stream=None):
+    """out[t] = sum_j expert_weights[t, j] * rows[inverse[t*k+j]]."""
+    dt, dev = _rows_dtype("rows", rows), _device()
+    T, H, R = cfg.num_tokens, cfg.hidden_dim, cfg.num_tokens * cfg.top_k
+    _check(load_library().moe_combine(
+        ctypes.byref(cfg), dt, _take(dev, "rows", rows, rows.dtype, R * H),
+        _take(dev, "inverse", inverse, torch.int32, R),
+        _take(dev, "expert_weights", expert_weights, torch.float32, R, False),
+        _take(dev, "out", out, rows.dtype, T * H), _stream(stream)), "moe_combine")
+
+
+def moe_combine_backward(cfg, d_out, inverse, d_rows, rows=None, expert_weights=None, d_expert_weights=None,
+                         stream=None):
+    """d_rows[inverse[t*k+j]] = expert_weights[t, j] * d_out[t] and, given rows,
+    d_expert_weights[t, j] = <d_out[t], rows[inverse[t*k+j]]>."""
+    dt, dev = _rows_dtype("d_out", d_out), _device()
+    T, H, R = cfg.num_tokens, cfg.hidden_dim, cfg.num_tokens * cfg.top_k
+    _check(load_library().moe_combine_backward(
+        ctypes.byref(cfg), dt, _take(dev, "d_out", d_out, d_out.dtype, T * H),
+        _take(dev, "rows", rows, d_out.dtype, R * H, d_expert_weights is not None),
+        _take(dev, "inverse", inverse, torch.int32, R),
+        _take(dev, "expert_weights", expert_weights, torch.float32, R, False),
+        _take(dev, "d_rows", d_rows, d_out.dtype, R * H),
+        _take(dev, "d_expert_weights", d_expert_weights, torch.float32, R, False), _stream(stream)),
+        "moe_combine_backward")
+
+
+def moe_route_backward(cfg, logits, expert_indices, d_expert_weights, d_logits, d_sink_weights=None,
+                       global_scale=None, d_global_scale=None, workspace=None, stream=None):
+    """d_logits [T, logits_row_stride] (and d_global_scale [1], which needs a
+    workspace of moe_operator_workspace_size) from the gradients of the
+    weights that moe_route returned for expert_indices."""
+    dev = _device()
+    T, k, S, n = cfg.num_tokens, cfg.top_k, cfg.num_sink, cfg.num_tokens * cfg.logits_row_stride
+    dt = torch.bfloat16 if cfg.logits_dtype == DTYPES[torch.bfloat16] else torch.float32
+    ws = None
+    if workspace is not None:
+        ws = _take(dev, "workspace", workspace, torch.uint8, workspace.numel())
+    _check(load_library().moe_route_backward(
+        ctypes.byref(cfg), _take(dev, "logits", logits, dt, n),
+        _take(dev, "global_scale", global_scale, torch.float32, 1, False),
+        _take(dev, "expert_indices", expert_indices, torch.int32, T * k),
+        _take(dev, "d_expert_weights", d_expert_weights, torch.float32, T * k),
+        _take(dev, "d_sink_weights", d_sink_weights, torch.float32, T * S, False),
+        _take(dev, "d_logits", d_logits, dt, n),
+        _take(dev, "d_global_scale", d_global_scale, torch.float32, 1, False), ws,
+        0 if workspace is None else workspace.numel(), _stream(stream)), "moe_route_backward")
+
+
+def moe_dispatch_int8(cfg, x, inverse, rows_q, row_scales, stream=None):
+    """moe_dispatch of bf16 tokens to 8-bit rows [T*k, int8_pitch(H)] and their scales [T*k]."""
+    dev = _device()
+    T, H, R = cfg.num_tokens, cfg.hidden_dim, cfg.num_tokens * cfg.top_k
+    _check(load_library().moe_dispatch_int8(
+        ctypes.byref(cfg), _take(dev, "x", x, torch.bfloat16, T * H), _take(dev, "inverse", inverse, torch.int32, R),
+        _take(dev, "rows_q", rows_q, torch.int8, R * int8_pitch(H)),
+        _take(dev, "row_scales", row_scales, torch.float32, R), _stream(stream)), "moe_dispatch_int8")
+
+
+def moe_quantize_rows(cfg, h, expert_offsets, rows_q, row_scales, stream=None):
+    """Activations h [T*k, D] bf16 to 8-bit rows [T*k, int8_pitch(D)] and their
+    scales, up to row expert_offsets[E] (None: all)."""
+    dev = _device()
+    D, R = cfg.moe_dim, cfg.num_tokens * cfg.top_k
+    _check(load_library().moe_quantize_rows(
+        ctypes.byref(cfg), _take(dev, "h", h, torch.bfloat16, R * D),
+        _take(dev, "expert_offsets", expert_offsets, torch.int32, cfg.num_experts + 1, False),
+        _take(dev, "rows_q", rows_q, torch.int8, R * int8_pitch(D)),
+        _take(dev, "row_scales", row_scales, torch.float32, R), _stream(stream)), "moe_quantize_rows")
+
+
+def _contraction(cfg, which):
+    """(code, K, N) of "gate_up" or "down"."""
+    if which not in CONTRACTIONS:
+        raise ValueError(f"contraction must be one of {sorted(CONTRACTIONS)}, not {which!r}")
+    if which == "gate_up":
+        return 0, cfg.hidden_dim, 2 * cfg.moe_dim
+    return 1, cfg.moe_dim, cfg.hidden_dim
+
+
+def moe_quantize_weights(cfg, contraction, w, w_q, w_scales, stream=None):
+    """Weights [E, K, N] bf16 of "gate_up" or "down" to [E, N, int8_pitch(K)]
+    8-bit and scales [E, N]: once, when the weights are loaded."""
+    (which, K, N), dev, E = _contraction(cfg, contraction), _device(), cfg.num_experts
+    _check(load_library().moe_quantize_weights(
+        ctypes.byref(cfg), which, _take(dev, "w", w, torch.bfloat16, E * K * N),
+        _take(dev, "w_q", w_q, torch.int8, E * N * int8_pitch(K)),
+        _take(dev, "w_scales", w_scales, torch.float32, E * N), _stream(stream)), "moe_quantize_weights")
+
+
+def moe_grouped_linear_int8(cfg, contraction, rows_q, row_scales, w_q, w_scales, expert_offsets, out, workspace,
+                            bias=None, stream=None):
+    """One contraction over rows sorted by expert, in 8-bit integers: "gate_up"
+    with the activation to out [T*k, D], "down" to out [T*k, H] (bf16)."""
+    (which, K, N), dev, E = _contraction(cfg, contraction), _device(), cfg.num_experts
+    R = cfg.num_tokens * cfg.top_k
+    _check(load_library().moe_grouped_linear_int8(
+        ctypes.byref(cfg), which, _take(dev, "rows_q", rows_q, torch.int8, R * int8_pitch(K)),
+        _take(dev, "row_scales", row_scales, torch.float32, R),
+        _take(dev, "w_q", w_q, torch.int8, E * N * int8_pitch(K)),
+        _take(dev, "w_scales", w_scales, torch.float32, E * N),
+        _take(dev, "bias", bias, torch.bfloat16, E * N, False),
+        _take(dev, "expert_offsets", expert_offsets, torch.int32, E + 1),
+        _take(dev, "out", out, torch.bfloat16, R * (cfg.hidden_dim if which else cfg.moe_dim)),
+        _take(dev, "workspace", workspace, torch.uint8, workspace.numel() if workspace is not None else 0),
+        workspace.numel(), _stream(stream)), "moe_grouped_linear_int8")
