@@ -198,7 +198,8 @@ def _p(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle of torch.cuda.current_stream(), without making the Stream object (3 us of a 4 us call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -367,19 +368,22 @@ def _take(device, name, t, dtype, numel, required=True):
         if required:
             raise ValueError(f"{name} is required")
         return None
+    if t.dtype is dtype and t.numel() == numel and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on the current CUDA device ({device}), not on {t.device}")
     if t.numel() != numel:
         raise ValueError(f"{name} must have {numel} elements, not {t.numel()}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be dense (contiguous)")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be dense (contiguous)")
 
 
 def _device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+    # (once CUDA is in use, the first test is all)
+    if torch.cuda.is_initialized() or torch.cuda.is_available():
+        return torch.cuda.current_device()
+    return -1
 
 
 def _rows_dtype(name, t):
