@@ -64,8 +64,23 @@ Tiling tiling(int vec) {
   return t;
 }
 
+// The positions (-1: no slot) and weights of KB of a token's slots, all loaded
+// before the first is used.
+template <int KB>
+__device__ __forceinline__ void load_slots(const RowsArgs& a, int64_t t, int j0, int (&p)[KB], float (&w)[KB]) {
+#pragma unroll
+  for (int q = 0; q < KB; ++q) {
+    const bool in = j0 + q < a.k;
+    p[q] = in ? __ldg(a.inverse + t * a.k + j0 + q) : -1;
+    w[q] = in && a.weights != nullptr ? __ldg(a.weights + t * a.k + j0 + q) : 1.f;
+  }
+#pragma unroll
+  for (int q = 0; q < KB; ++q)
+    if (p[q] >= a.R) p[q] = -1;
+}
+
 // rows[p] = w * tok[t] for each of the token's slots.
-template <bool F32>
+template <bool F32, int KB>
 __global__ void __launch_bounds__(kRowThreads) spread_kernel(const RowsArgs a, int cw_log, int chunks) {
   griddep_wait();  // the previous kernel's results are complete and visible
   griddep_launch_dependents();
@@ -74,26 +89,29 @@ __global__ void __launch_bounds__(kRowThreads) spread_kernel(const RowsArgs a, i
   const int64_t t = (static_cast<int64_t>(tile) << (8 - cw_log)) + (threadIdx.x >> cw_log);
   if (t >= a.T || c >= a.vec) return;
   const uint4 u = __ldg(static_cast<const uint4*>(a.tok_in) + t * a.vec + c);
-  uint4* rows = static_cast<uint4*>(a.rows_out);
+  uint4* rows = static_cast<uint4*>(a.rows_out) + c;
   Vec<F32> x;
   x.unpack(u);
-  for (int j = 0; j < a.k; ++j) {
-    const int p = __ldg(a.inverse + t * a.k + j);
-    if (p < 0 || p >= a.R) continue;
-    uint4 o = u;
-    if (a.weights != nullptr) {
-      const float w = __ldg(a.weights + t * a.k + j);
-      Vec<F32> y;
+  for (int j0 = 0; j0 < a.k; j0 += KB) {
+    int p[KB];
+    float w[KB];
+    load_slots<KB>(a, t, j0, p, w);
 #pragma unroll
-      for (int i = 0; i < Vec<F32>::N; ++i) y.v[i] = w * x.v[i];
-      o = y.pack();
+    for (int q = 0; q < KB; ++q) {
+      uint4 o = u;
+      if (a.weights != nullptr) {
+        Vec<F32> y;
+#pragma unroll
+        for (int i = 0; i < Vec<F32>::N; ++i) y.v[i] = w[q] * x.v[i];
+        o = y.pack();
+      }
+      if (p[q] >= 0) rows[static_cast<int64_t>(p[q]) * a.vec] = o;
     }
-    rows[static_cast<int64_t>(p) * a.vec + c] = o;
   }
 }
 
 // out[t] = sum_j w * rows[p], j ascending in fp32.
-template <bool F32>
+template <bool F32, int KB>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsArgs a, int cw_log, int chunks) {
   griddep_wait();  // the previous kernel's results are complete and visible
   griddep_launch_dependents();
@@ -101,28 +119,21 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsArgs a, i
   const int c = static_cast<int>(((blockIdx.x - tile * chunks) << cw_log) + (threadIdx.x & ((1u << cw_log) - 1u)));
   const int64_t t = (static_cast<int64_t>(tile) << (8 - cw_log)) + (threadIdx.x >> cw_log);
   if (t >= a.T || c >= a.vec) return;
-  const uint4* rows = static_cast<const uint4*>(a.rows_in);
+  const uint4* rows = static_cast<const uint4*>(a.rows_in) + c;
   Vec<F32> acc;
 #pragma unroll
   for (int i = 0; i < Vec<F32>::N; ++i) acc.v[i] = 0.f;
-  constexpr int kBatch = 8;  // rows in flight before the first is added
-  for (int j0 = 0; j0 < a.k; j0 += kBatch) {
-    uint4 u[kBatch];
-    float w[kBatch];
-    bool on[kBatch];
+  for (int j0 = 0; j0 < a.k; j0 += KB) {
+    int p[KB];
+    float w[KB];
+    uint4 u[KB];
+    load_slots<KB>(a, t, j0, p, w);
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const int j = j0 + q;
-      const int p = j < a.k ? __ldg(a.inverse + t * a.k + j) : -1;
-      on[q] = p >= 0 && p < a.R;
-      if (on[q]) {
-        u[q] = __ldg(rows + static_cast<int64_t>(p) * a.vec + c);
-        w[q] = a.weights != nullptr ? __ldg(a.weights + t * a.k + j) : 1.f;
-      }
-    }
+    for (int q = 0; q < KB; ++q)
+      if (p[q] >= 0) u[q] = __ldg(rows + static_cast<int64_t>(p[q]) * a.vec);
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      if (on[q]) {
+    for (int q = 0; q < KB; ++q) {
+      if (p[q] >= 0) {
         Vec<F32> y;
         y.unpack(u[q]);
 #pragma unroll
@@ -219,17 +230,24 @@ cudaError_t launch_dot(const RowsArgs& a, cudaStream_t stream) {
   return launch_pdl(rows_dot_kernel<F32, SPREAD, 32>, grid, block, 0, stream, a);
 }
 
-template <bool F32>
-cudaError_t launch_rows(const RowsArgs& a, bool spread, cudaStream_t stream) {
-  if (a.d_weights != nullptr)
-    return spread ? launch_dot<F32, true>(a, stream) : launch_dot<F32, false>(a, stream);
+template <bool F32, int KB>
+cudaError_t launch_copy(const RowsArgs& a, bool spread, cudaStream_t stream) {
   const Tiling tl = tiling(a.vec);
   const int per_block = kRowThreads >> tl.cw_log;
   const int64_t blocks = (static_cast<int64_t>(a.T) + per_block - 1) / per_block * tl.chunks;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  if (spread) return launch_pdl(spread_kernel<F32>, grid, dim3(kRowThreads), 0, stream, a, tl.cw_log, tl.chunks);
-  return launch_pdl(gather_kernel<F32>, grid, dim3(kRowThreads), 0, stream, a, tl.cw_log, tl.chunks);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kRowThreads);
+  if (spread) return launch_pdl(spread_kernel<F32, KB>, grid, block, 0, stream, a, tl.cw_log, tl.chunks);
+  return launch_pdl(gather_kernel<F32, KB>, grid, block, 0, stream, a, tl.cw_log, tl.chunks);
+}
+
+template <bool F32>
+cudaError_t launch_rows(const RowsArgs& a, bool spread, cudaStream_t stream) {
+  if (a.d_weights != nullptr)
+    return spread ? launch_dot<F32, true>(a, stream) : launch_dot<F32, false>(a, stream);
+  if (a.k <= 2) return launch_copy<F32, 2>(a, spread, stream);
+  if (a.k <= 4) return launch_copy<F32, 4>(a, spread, stream);
+  return launch_copy<F32, 8>(a, spread, stream);
 }
 
 }  // namespace
