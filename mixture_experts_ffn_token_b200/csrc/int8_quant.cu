@@ -54,23 +54,25 @@ __device__ __forceinline__ uint2 quant8(const uint4& u, const Quant& q) {
       pack4(q_bits(bf16_lo(u.z), q), q_bits(bf16_hi(u.z), q), q_bits(bf16_lo(u.w), q), q_bits(bf16_hi(u.w), q)));
 }
 
-// One block per row, 16 values a thread and step; the row stays in registers
-// between the maximum and the rounding (up to kHeld steps), so it is read
-// once and its k copies are written once each.
+// 2^g_log threads per row (a warp at least, 256 / 2^g_log rows a block), 16
+// values a thread and step; the row stays in registers between the maximum
+// and the rounding (up to kHeld steps), so it is read once and its k copies
+// are written once each.
 constexpr int kHeld = 2;
 constexpr int kQuantThreads = 512;
 
-__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv_bfloat16* __restrict__ in, int n,
+__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv_bfloat16* __restrict__ in, int rows,
+                                                                      int n, int g_log,
                                                                       const int32_t* __restrict__ inverse, int k,
                                                                       int R, const int32_t* __restrict__ total,
                                                                       int8_t* __restrict__ q,
                                                                       float* __restrict__ scales) {
   griddep_wait();  // the previous kernel's results are complete and visible
   griddep_launch_dependents();
-  const int64_t row = blockIdx.x;
-  if (total != nullptr && row >= *total) return;
-  const int tid = threadIdx.x, steps = blockDim.x;
-  const int chunks = (n + 15) / 16, vec = n / 8;
+  const int steps = 1 << g_log, tid = threadIdx.x & (steps - 1), group = threadIdx.x >> g_log;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> g_log) + group;
+  const bool live = row < rows && (total == nullptr || row < *total);
+  const int chunks = (n + 15) / 16, vec = live ? n / 8 : 0;  // nothing is read of a row that is not live
   const uint4* src = reinterpret_cast<const uint4*>(in + row * n);
   const uint4 zero = make_uint4(0, 0, 0, 0);
   uint4 a[kHeld], b[kHeld];
@@ -83,16 +85,19 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv
   }
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) m = absmax8(absmax8(m, a[i]), b[i]);
-  for (int c = tid + kHeld * steps; c < chunks; c += steps) {
+  for (int c = tid + kHeld * steps; 2 * c < vec; c += steps) {
     m = absmax8(m, __ldg(src + 2 * c));
     if (2 * c + 1 < vec) m = absmax8(m, __ldg(src + 2 * c + 1));
   }
   m = max(m & 0xffffu, m >> 16);
   m = __reduce_max_sync(0xffffffffu, m);
-  __shared__ uint32_t s_max[kQuantThreads / 32];
-  if ((tid & 31) == 0) s_max[tid >> 5] = m;
-  __syncthreads();
-  for (int w = 0; w < (steps >> 5); ++w) m = max(m, s_max[w]);
+  if (steps > 32) {
+    __shared__ uint32_t s_max[kQuantThreads / 32];
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+    __syncthreads();
+    for (int w = 0; w < (steps >> 5); ++w) m = max(m, s_max[group * (steps >> 5) + w]);
+  }
+  if (!live) return;
   const Quant qt = quant_of(m);
   const int64_t pitch = 16 * static_cast<int64_t>(chunks);
   auto store = [&](int c, const uint4& va, const uint4& vb) {
@@ -204,10 +209,14 @@ __global__ void __launch_bounds__(kWThreads) quantize_weights_kernel(const __nv_
 cudaError_t launch_quantize_rows(const __nv_bfloat16* in, int rows, int n, const int32_t* inverse, int k, int R,
                                  const int32_t* total, int8_t* q, float* scales, cudaStream_t stream) {
   if (rows == 0) return cudaSuccess;
+  // as many threads as hold the row in registers
   const int chunks = (n + 15) / 16;
-  const int threads = std::min(kQuantThreads, (chunks + 31) / 32 * 32);
-  return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>(rows)), dim3(static_cast<unsigned>(threads)), 0,
-                    stream, in, n, inverse, k, R, total, q, scales);
+  int g_log = 5;
+  while ((1 << g_log) * kHeld < chunks && (1 << g_log) < kQuantThreads) ++g_log;
+  const int threads = std::max(256, 1 << g_log), per_block = threads >> g_log;
+  return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)),
+                    dim3(static_cast<unsigned>(threads)), 0, stream, in, rows, n, g_log, inverse, k, R, total, q,
+                    scales);
 }
 
 cudaError_t launch_quantize_weights(const __nv_bfloat16* w, int E, int K, int N, int8_t* q, float* scales,
