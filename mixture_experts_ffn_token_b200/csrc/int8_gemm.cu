@@ -97,58 +97,78 @@ __device__ __forceinline__ float gated(int act, float g, float u, float alpha, f
   return __fdividef(g, 1.f + __expf(-1.5957691216057308f * (g + 0.044715f * g * g * g))) * u;
 }
 
-// Four consecutive columns' scales and biases (zero past the columns' end).
+// An epilogue warp's 128 weight columns of a tile: their scales lie in the 16
+// bytes that the rows of its staging block leave free (columns 4i .. 4i+3 in
+// row i), their biases behind the block.  Column 4i is `cols(i)` of the
+// expert's N columns; the loads are issued while the tile's product is still
+// running, since the scales come from HBM.
+constexpr int kWarpStage = kStageWarpBytes + 256;
+
+// First weight column of the warp's group i of four, or -1 past the end.
+template <int MODE>
+__device__ __forceinline__ int group_col(const Int8Params& p, const TileCoord& tc, int part, int i) {
+  if constexpr (MODE == MODE_CONCAT) {  // 64 gate columns, then the 64 matching up columns
+    const int h = tc.n * 128 + part * 64 + 4 * (i & 15);
+    return h < p.out_cols ? (i >> 4) * p.out_cols + h : -1;
+  } else {
+    const int c = tc.n * BN + part * 128 + 4 * i;
+    return c < p.N ? c : -1;
+  }
+}
+
+template <int MODE>
+__device__ __forceinline__ void stage_columns(const Int8Params& p, const TileCoord& tc, int part, int lane,
+                                              uint8_t* stage) {
+  const int c = group_col<MODE>(p, tc, part, lane);
+  const int64_t base = static_cast<int64_t>(tc.e) * p.N;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  uint2 b = make_uint2(0u, 0u);
+  if (c >= 0) {
+    s = __ldg(reinterpret_cast<const float4*>(p.w_scales + base + c));
+    if (p.bias != nullptr) b = __ldg(reinterpret_cast<const uint2*>(p.bias + base + c));
+  }
+  __syncwarp();  // every lane is done with the tile before
+  *reinterpret_cast<float4*>(stage + lane * kStageRowBytes + 64) = s;
+  *reinterpret_cast<uint2*>(stage + kStageWarpBytes + 8 * lane) = b;
+  __syncwarp();
+}
+
 struct Col4 {
   float s[4], b[4];
 };
-__device__ __forceinline__ Col4 load_cols(const Int8Params& p, int64_t base, int col, int limit) {
-  Col4 c;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  uint2 b = make_uint2(0u, 0u);
-  if (col < limit) {
-    s = __ldg(reinterpret_cast<const float4*>(p.w_scales + base + col));
-    if (p.bias != nullptr) b = __ldg(reinterpret_cast<const uint2*>(p.bias + base + col));
-  }
-  c.s[0] = s.x;
-  c.s[1] = s.y;
-  c.s[2] = s.z;
-  c.s[3] = s.w;
-  c.b[0] = bf16_lo(b.x);
-  c.b[1] = bf16_hi(b.x);
-  c.b[2] = bf16_lo(b.y);
-  c.b[3] = bf16_hi(b.y);
-  return c;
+__device__ __forceinline__ Col4 columns(const uint8_t* stage, int i) {
+  const float4 s = *reinterpret_cast<const float4*>(stage + i * kStageRowBytes + 64);
+  const uint2 b = *reinterpret_cast<const uint2*>(stage + kStageWarpBytes + 8 * i);
+  return {{s.x, s.y, s.z, s.w}, {bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y)}};
 }
 
 __device__ __forceinline__ float scaled(uint32_t acc, float row, const Col4& c, int i) {
   return fmaf(static_cast<float>(static_cast<int>(acc)) * row, c.s[i], c.b[i]);
 }
 
-// 32 output columns (tile column oc on) of this thread's row, packed to bf16.
+// 32 output columns of this thread's row, from column `rel` of the warp's part
+// of the tile (accumulator columns from tacc on), packed to bf16.
 template <int MODE>
-__device__ __forceinline__ void out_chunk(const Int8Params& p, const TileCoord& tc, uint32_t tacc, int oc, float row,
-                                          uint32_t (&packed)[16]) {
-  const int64_t base = static_cast<int64_t>(tc.e) * p.N;
+__device__ __forceinline__ void out_chunk(const Int8Params& p, uint32_t tacc, int part, int rel, float row,
+                                          const uint8_t* stage, uint32_t (&packed)[16]) {
   if constexpr (MODE == MODE_DOWN) {
-    const int col0 = tc.n * BN + oc;
     uint32_t a[32];
-    tmem_ld32(tacc + oc, a);
+    tmem_ld32(tacc + part * 128 + rel, a);
     tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-      const Col4 c = load_cols(p, base, col0 + j, p.N);
+      const Col4 c = columns(stage, (rel + j) >> 2);
       packed[j / 2] = pack_bf16x2(scaled(a[j], row, c, 0), scaled(a[j + 1], row, c, 1));
       packed[j / 2 + 1] = pack_bf16x2(scaled(a[j + 2], row, c, 2), scaled(a[j + 3], row, c, 3));
     }
   } else if constexpr (MODE == MODE_CONCAT) {
-    const int col0 = tc.n * 128 + oc, D = p.out_cols;
     uint32_t g[32], u[32];
-    tmem_ld32(tacc + oc, g);
-    tmem_ld32(tacc + 128 + oc, u);
+    tmem_ld32(tacc + part * 64 + rel, g);
+    tmem_ld32(tacc + 128 + part * 64 + rel, u);
     tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-      const Col4 cg = load_cols(p, base, col0 + j, D), cu = load_cols(p, base + D, col0 + j, D);
+      const Col4 cg = columns(stage, (rel + j) >> 2), cu = columns(stage, 16 + ((rel + j) >> 2));
       float h[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -157,14 +177,13 @@ __device__ __forceinline__ void out_chunk(const Int8Params& p, const TileCoord& 
       packed[j / 2 + 1] = pack_bf16x2(h[2], h[3]);
     }
   } else {
-    const int col0 = 2 * (tc.n * 128 + oc);
     uint32_t a[64];
-    tmem_ld32(tacc + 2 * oc, a);
-    tmem_ld32(tacc + 2 * oc + 32, a + 32);
+    tmem_ld32(tacc + part * 128 + 2 * rel, a);
+    tmem_ld32(tacc + part * 128 + 2 * rel + 32, a + 32);
     tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 64; j += 4) {
-      const Col4 c = load_cols(p, base, col0 + j, p.N);
+      const Col4 c = columns(stage, (2 * rel + j) >> 2);
       const float h0 = gated(p.activation, scaled(a[j], row, c, 0), scaled(a[j + 1], row, c, 1), p.alpha, p.limit);
       const float h1 = gated(p.activation, scaled(a[j + 2], row, c, 2), scaled(a[j + 3], row, c, 3), p.alpha, p.limit);
       packed[j / 4] = pack_bf16x2(h0, h1);
@@ -173,31 +192,29 @@ __device__ __forceinline__ void out_chunk(const Int8Params& p, const TileCoord& 
 }
 
 // One tile's epilogue for one warp (TMEM lane quadrant `quad`, half `part` of
-// the tile's output columns).  half: the M = 64 accumulator holds row r in
-// lane 32*(r/16) + r%16.  Each 32 x 32 block is turned through the staging
-// block so that a store instruction writes 8 rows x 64 contiguous bytes.
+// the tile's output columns), rs its thread's row scale.  half: the M = 64
+// accumulator holds row r in lane 32*(r/16) + r%16.  Each 32 x 32 block is
+// turned through the staging block so that a store instruction writes 8 rows
+// x 64 contiguous bytes.
 template <int MODE>
 __device__ __forceinline__ void epilogue(const Int8Params& p, const TileCoord& tc, uint32_t tacc, int quad, int part,
-                                         int lane, uint8_t* stage, bool half) {
-  const int row = half ? quad * 16 + lane : quad * 32 + lane;
-  const bool has_row = (!half || lane < 16) && row < tc.rows;
-  const float rs = has_row ? __ldg(p.a_scales + tc.row0 + row) : 0.f;
-  constexpr int kTileCols = MODE == MODE_DOWN ? BN : BN / 2;
-  const int rel0 = part * (kTileCols / 2);
+                                         int lane, float rs, uint8_t* stage, bool half) {
+  constexpr int kPartCols = MODE == MODE_DOWN ? BN / 2 : BN / 4;  // output columns of the warp
+  const int col0 = tc.n * 2 * kPartCols + part * kPartCols;
   const int q = lane & 3;
   uint8_t* my_row = stage + lane * kStageRowBytes;
 #pragma unroll 1
-  for (int rel = rel0; rel < rel0 + kTileCols / 2; rel += kOutChunk) {
-    if (tc.n * kTileCols + rel >= p.out_cols) break;
+  for (int rel = 0; rel < kPartCols; rel += kOutChunk) {
+    if (col0 + rel >= p.out_cols) break;
     uint32_t packed[16];
-    out_chunk<MODE>(p, tc, tacc, rel, rs, packed);
+    out_chunk<MODE>(p, tacc, part, rel, rs, stage, packed);
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       *reinterpret_cast<uint4*>(my_row + 16 * c) =
           make_uint4(packed[4 * c], packed[4 * c + 1], packed[4 * c + 2], packed[4 * c + 3]);
     __syncwarp();
-    const int col = tc.n * kTileCols + rel + 8 * q;
+    const int col = col0 + rel + 8 * q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int l = 8 * i + (lane >> 2);  // the lane whose row this is
@@ -380,16 +397,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // -------------------------------------------------------- epilogue
     const int quad = warp & 3;         // this warp may access TMEM lanes 32*quad..+31
     const int part = (warp - 2) >> 2;  // which half of the tile's columns
-    uint8_t* stage = s_stage + (warp - 2) * kStageWarpBytes;
+    uint8_t* stage = s_stage + (warp - 2) * kWarpStage;
     int ti = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
       const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
       const int acc = ti & 1;
+      const bool half = tc.rows <= HALF_ROWS;
+      const int row = half ? quad * 16 + lane : quad * 32 + lane;
+      const float rs = (!half || lane < 16) && row < tc.rows ? __ldg(p.a_scales + tc.row0 + row) : 0.f;
+      stage_columns<MODE>(p, tc, part, lane, stage);
       const bool got = mbar_wait(tfull0 + 8 * acc, static_cast<uint32_t>(ti >> 1) & 1u, abort_flag, kTimeoutNs);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after_sync();
       const uint32_t tacc = tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quad * 32) << 16);
-      epilogue<MODE>(p, tc, tacc, quad, part, lane, stage, tc.rows <= HALF_ROWS);
+      epilogue<MODE>(p, tc, tacc, quad, part, lane, rs, stage, half);
       tc_fence_before_sync();
       mbar_arrive(tempty0 + 8 * acc);
     }
@@ -407,7 +428,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 constexpr size_t smem_bytes(int E) {
   return 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + CTRL_BYTES + 2 * static_cast<size_t>(E + 1) * 4 + 16 +
-         NUM_EPI_WARPS * kStageWarpBytes;
+         NUM_EPI_WARPS * kWarpStage;
 }
 
 template <int MODE>
