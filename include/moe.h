@@ -379,7 +379,8 @@ moe_status_t moe_operator_workspace_size(const moe_config_t* cfg, size_t* bytes)
  *   d_sink_weights    [T, S] fp32 or NULL for zero; NULL when S = 0.
  *   d_logits          [T, logits_row_stride] of logits_dtype out: columns
  *                     0 .. E+S-1 overwritten (zero where nothing was
- *                     selected), the tail of a wider row left as it was.
+ *                     selected), the tail of a wider row left as it was; it
+ *                     must not overlap the inputs.
  *   d_global_scale    [1] fp32 out or NULL; SIGMOID_SINK only.
  *   workspace         moe_operator_workspace_size(), only with d_global_scale
  *                     (else it may be NULL).
