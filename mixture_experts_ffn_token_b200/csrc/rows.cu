@@ -147,23 +147,18 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsArgs a, i
 // The same with the weights' gradient: one block per token, its k inner
 // products reduced over the block in a fixed order.  SPREAD: rows[p] =
 // w * tok[t] is written; else out[t] = sum_j w * rows[p] (KB >= k terms, kept
-// in registers so that every row is read once).
-template <bool F32, bool SPREAD, int KB>
+// in registers so that every row is read once).  A thread loads U columns of
+// up to 8 / U rows before it uses the first.
+template <bool F32, bool SPREAD, int KB, int U>
 __global__ void __launch_bounds__(kRowThreads) rows_dot_kernel(const RowsArgs a) {
   griddep_wait();  // the previous kernel's results are complete and visible
   griddep_launch_dependents();
-  __shared__ int s_p[KB];
-  __shared__ float s_w[KB];
   __shared__ float s_part[kRowThreads / 32][KB];
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int j = tid; j < KB; j += blockDim.x) {
-    int p = j < a.k ? a.inverse[t * a.k + j] : -1;
-    if (p >= a.R) p = -1;
-    s_p[j] = p;
-    s_w[j] = j < a.k && a.weights != nullptr ? a.weights[t * a.k + j] : 1.f;
-  }
-  __syncthreads();
+  int p[KB];
+  float w[KB];
+  load_slots<KB>(a, t, 0, p, w);
   const uint4* tok = static_cast<const uint4*>(a.tok_in) + t * a.vec;
   const uint4* rows = static_cast<const uint4*>(a.rows_in);
   constexpr int N = Vec<F32>::N;
@@ -171,36 +166,57 @@ __global__ void __launch_bounds__(kRowThreads) rows_dot_kernel(const RowsArgs a)
   float dot[KB];
 #pragma unroll
   for (int j = 0; j < KB; ++j) dot[j] = 0.f;
-  for (int c = tid; c < a.vec; c += blockDim.x) {
-    Vec<F32> x, acc;
-    x.unpack(__ldg(tok + c));
+  for (int c0 = tid; c0 < a.vec; c0 += U * blockDim.x) {
+    uint4 ux[U];
+    Vec<F32> x[U], acc[U];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc.v[i] = 0.f;
+    for (int v = 0; v < U; ++v) {
+      const int c = c0 + v * blockDim.x;
+      ux[v] = c < a.vec ? __ldg(tok + c) : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int j0 = 0; j0 < KB; j0 += kBatch) {
-      uint4 u[kBatch];
+      uint4 u[U][kBatch];
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        const int p = s_p[j0 + q];
-        if (p >= 0) u[q] = __ldg(rows + static_cast<int64_t>(p) * a.vec + c);
+      for (int v = 0; v < U; ++v) {
+        const int c = c0 + v * blockDim.x;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+          u[v][q] = p[j0 + q] >= 0 && c < a.vec ? __ldg(rows + static_cast<int64_t>(p[j0 + q]) * a.vec + c)
+                                                : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        const int p = s_p[j0 + q];
-        if (p < 0) continue;
-        const float w = s_w[j0 + q];
-        Vec<F32> y, o;
-        y.unpack(u[q]);
+      for (int v = 0; v < U; ++v) {
+        const int c = c0 + v * blockDim.x;
+        if (j0 == 0) {
+          x[v].unpack(ux[v]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          dot[j0 + q] += x.v[i] * y.v[i];
-          if constexpr (SPREAD) o.v[i] = w * x.v[i];
-          else acc.v[i] += w * y.v[i];
+          for (int i = 0; i < N; ++i) acc[v].v[i] = 0.f;
         }
-        if constexpr (SPREAD) static_cast<uint4*>(a.rows_out)[static_cast<int64_t>(p) * a.vec + c] = o.pack();
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          if (p[j0 + q] < 0) continue;
+          Vec<F32> y, o;
+          y.unpack(u[v][q]);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            dot[j0 + q] += x[v].v[i] * y.v[i];
+            if constexpr (SPREAD) o.v[i] = w[j0 + q] * x[v].v[i];
+            else acc[v].v[i] += w[j0 + q] * y.v[i];
+          }
+          if constexpr (SPREAD) {
+            if (c < a.vec) static_cast<uint4*>(a.rows_out)[static_cast<int64_t>(p[j0 + q]) * a.vec + c] = o.pack();
+          }
+        }
       }
     }
-    if constexpr (!SPREAD) static_cast<uint4*>(a.tok_out)[t * a.vec + c] = acc.pack();
+    if constexpr (!SPREAD) {
+#pragma unroll
+      for (int v = 0; v < U; ++v) {
+        const int c = c0 + v * blockDim.x;
+        if (c < a.vec) static_cast<uint4*>(a.tok_out)[t * a.vec + c] = acc[v].pack();
+      }
+    }
   }
 #pragma unroll
   for (int j = 0; j < KB; ++j) {
@@ -212,22 +228,30 @@ __global__ void __launch_bounds__(kRowThreads) rows_dot_kernel(const RowsArgs a)
   __syncthreads();
   const int warps = blockDim.x >> 5;
   for (int j = tid; j < a.k; j += blockDim.x) {
+    const int pj = a.inverse[t * a.k + j];
     float v = 0.f;
-    for (int w = 0; w < warps; ++w) v += s_part[w][j];
-    a.d_weights[t * a.k + j] = s_p[j] >= 0 ? v : 0.f;
+    for (int i = 0; i < warps; ++i) v += s_part[i][j];
+    a.d_weights[t * a.k + j] = pj >= 0 && pj < a.R ? v : 0.f;
   }
+}
+
+template <bool F32, bool SPREAD, int KB, int U>
+cudaError_t launch_dot_k(const RowsArgs& a, cudaStream_t stream) {
+  int threads = 32;
+  while (threads < kRowThreads && threads * U < a.vec) threads <<= 1;
+  return launch_pdl(rows_dot_kernel<F32, SPREAD, KB, U>, dim3(static_cast<unsigned>(a.T)),
+                    dim3(static_cast<unsigned>(threads)), 0, stream, a);
 }
 
 template <bool F32, bool SPREAD>
 cudaError_t launch_dot(const RowsArgs& a, cudaStream_t stream) {
-  int threads = 32;
-  while (threads < kRowThreads && threads < a.vec) threads <<= 1;
-  const dim3 grid(static_cast<unsigned>(a.T)), block(static_cast<unsigned>(threads));
-  if (a.k <= 2) return launch_pdl(rows_dot_kernel<F32, SPREAD, 2>, grid, block, 0, stream, a);
-  if (a.k <= 4) return launch_pdl(rows_dot_kernel<F32, SPREAD, 4>, grid, block, 0, stream, a);
-  if (a.k <= 8) return launch_pdl(rows_dot_kernel<F32, SPREAD, 8>, grid, block, 0, stream, a);
-  if (a.k <= 16) return launch_pdl(rows_dot_kernel<F32, SPREAD, 16>, grid, block, 0, stream, a);
-  return launch_pdl(rows_dot_kernel<F32, SPREAD, 32>, grid, block, 0, stream, a);
+  if (a.k <= 1) return launch_dot_k<F32, SPREAD, 1, 4>(a, stream);
+  if (a.k <= 2) return launch_dot_k<F32, SPREAD, 2, 4>(a, stream);
+  if (a.k <= 4) return launch_dot_k<F32, SPREAD, 4, 2>(a, stream);
+  if (a.k <= 6) return launch_dot_k<F32, SPREAD, 6, 1>(a, stream);
+  if (a.k <= 8) return launch_dot_k<F32, SPREAD, 8, 1>(a, stream);
+  if (a.k <= 16) return launch_dot_k<F32, SPREAD, 16, 1>(a, stream);
+  return launch_dot_k<F32, SPREAD, 32, 1>(a, stream);
 }
 
 template <bool F32, int KB>
