@@ -195,6 +195,7 @@ struct RowsArgs {
   const float* weights;    // [R] or null for 1
   float* d_weights;        // [R] or null
   int T, k, R, vec;
+  int num_sms;
 };
 cudaError_t launch_rows_spread(const RowsArgs& a, bool f32, cudaStream_t stream);
 cudaError_t launch_rows_gather(const RowsArgs& a, bool f32, cudaStream_t stream);

@@ -35,7 +35,8 @@ moe_status_t check_rows(const moe_config_t* cfg, moe_dtype_t dtype, const int32_
 bool given(const void* p) { return p != nullptr && aligned16(p); }
 bool given_or_null(const void* p) { return aligned16(p); }
 
-moe::RowsArgs rows_args(const moe_config_t* c, moe_dtype_t dtype, const int32_t* inverse, const float* weights) {
+moe::RowsArgs rows_args(const moe_config_t* c, moe_dtype_t dtype, const int32_t* inverse, const float* weights,
+                        int num_sms) {
   moe::RowsArgs a = {};
   a.inverse = inverse;
   a.weights = weights;
@@ -43,6 +44,7 @@ moe::RowsArgs rows_args(const moe_config_t* c, moe_dtype_t dtype, const int32_t*
   a.k = c->top_k;
   a.R = c->num_tokens * c->top_k;
   a.vec = c->hidden_dim / (dtype == MOE_DTYPE_F32 ? 4 : 8);  // hidden_dim is a multiple of 8
+  a.num_sms = num_sms;
   return a;
 }
 
@@ -88,7 +90,7 @@ moe_status_t moe_dispatch(const moe_config_t* cfg, moe_dtype_t dtype, const void
   if (!given(x) || !given(rows)) return MOE_ERR_INVALID_ARGUMENT;
   int num_sms = 0;
   if ((st = current_device(&num_sms)) != MOE_OK) return st;
-  moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights);
+  moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights, num_sms);
   a.tok_in = x;
   a.rows_out = rows;
   return cuda_status(moe::launch_rows_spread(a, dtype == MOE_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)));
@@ -106,7 +108,7 @@ moe_status_t moe_dispatch_backward(const moe_config_t* cfg, moe_dtype_t dtype, c
   if (d_expert_weights != nullptr && x == nullptr) return MOE_ERR_INVALID_ARGUMENT;
   int num_sms = 0;
   if ((st = current_device(&num_sms)) != MOE_OK) return st;
-  moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights);
+  moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights, num_sms);
   a.rows_in = d_rows;
   a.tok_in = x;
   a.tok_out = d_x;
@@ -124,7 +126,7 @@ moe_status_t moe_combine(const moe_config_t* cfg, moe_dtype_t dtype, const void*
   if (!given(rows) || !given(out)) return MOE_ERR_INVALID_ARGUMENT;
   int num_sms = 0;
   if ((st = current_device(&num_sms)) != MOE_OK) return st;
-  moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights);
+  moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights, num_sms);
   a.rows_in = rows;
   a.tok_out = out;
   return cuda_status(moe::launch_rows_gather(a, dtype == MOE_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)));
@@ -142,7 +144,7 @@ moe_status_t moe_combine_backward(const moe_config_t* cfg, moe_dtype_t dtype, co
   if (d_expert_weights != nullptr && rows == nullptr) return MOE_ERR_INVALID_ARGUMENT;
   int num_sms = 0;
   if ((st = current_device(&num_sms)) != MOE_OK) return st;
-  moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights);
+  moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights, num_sms);
   a.tok_in = d_out;
   a.rows_in = rows;
   a.rows_out = d_rows;

@@ -127,12 +127,14 @@ def _all_rows(cfg, x, rows, w, inv, T, H, k):
     return spread, out, d_x, d_w1, d_rows, d_w2
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
-def test_rows_large(dtype):
+@pytest.mark.parametrize("T,H,E,k,drop,dtype", [
+    (5003, 1544, 128, 6, 0.0, BF16), (5003, 1544, 128, 6, 0.0, F32), (8209, 4104, 8, 2, 0.0, BF16),
+    (1100, 2056, 40, 3, 0.3, F32), (1025, 1000, 30, 16, 0.1, BF16), (4097, 2184, 16, 8, 0.2, BF16),
+    (12007, 264, 9, 4, 0.1, BF16), (16500, 24, 3, 1, 0.0, F32)])
+def test_rows_large(T, H, E, k, drop, dtype):
     """Tokens by the thousand, ragged, the same bits on every run."""
-    T, H, E, k = 5003, 1544, 128, 6
     cfg = abi.config(T, H, E, k, 8)
-    _, _, inv = R.routing(T, E, k, seed=11)
+    _, off, inv = R.routing(T, E, k, seed=11, drop=drop)
     x, rows, w = randn(1, T, H, dtype=dtype), randn(2, T * k, H, dtype=dtype), randn(3, T, k)
     a = _all_rows(cfg, x.cuda(), rows.cuda(), w.cuda(), inv.cuda(), T, H, k)
     b = _all_rows(cfg, x.cuda(), rows.cuda(), w.cuda(), inv.cuda(), T, H, k)
