@@ -446,6 +446,17 @@ bool use_ring(const RowsArgs& a) {
   return a.k >= 3 && a.k <= 16 && a.T >= 1024 && bytes >= (int64_t(24) << 20);
 }
 
+template <bool F32, bool SPREAD>
+cudaError_t launch_dot(const RowsArgs& a, cudaStream_t stream) {
+  if (a.k <= 1) return launch_dot_k<F32, SPREAD, 1, 4>(a, stream);
+  if (a.k <= 2) return launch_dot_k<F32, SPREAD, 2, 4>(a, stream);
+  if (a.k <= 4) return launch_dot_k<F32, SPREAD, 4, 2>(a, stream);
+  if (a.k <= 6) return launch_dot_k<F32, SPREAD, 6, 1>(a, stream);
+  if (a.k <= 8) return launch_dot_k<F32, SPREAD, 8, 1>(a, stream);
+  if (a.k <= 16) return launch_dot_k<F32, SPREAD, 16, 1>(a, stream);
+  return launch_dot_k<F32, SPREAD, 32, 1>(a, stream);
+}
+
 template <bool F32, int KB, int U>
 cudaError_t launch_copy(const RowsArgs& a, bool spread, cudaStream_t stream) {
   const Tiling tl = tiling(a.vec, spread ? 1 : U);
