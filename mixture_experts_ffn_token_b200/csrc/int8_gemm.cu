@@ -38,12 +38,12 @@ constexpr int A_BYTES = BM * BK;           // 16 KB
 constexpr int B_BYTES = BN * BK;           // 32 KB
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 4;
-constexpr int HALF_ROWS = 64;
-constexpr int HALF_A_BYTES = HALF_ROWS * BK;
+constexpr int HALF_ROWS = 64;              // tiles of at most 64 rows: M = 64
+constexpr int FEW_ROWS = 16;               // tiles that copy only 16 rows of A
 constexpr int NUM_EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + 32 * NUM_EPI_WARPS;
-constexpr uint32_t TMEM_COLS = 512;
 constexpr int CTRL_BYTES = 256;
+constexpr uint32_t TMEM_COLS = 2 * BN;     // two accumulators
 
 // Instruction descriptor for kind::i8, signed A and B, both K-major, 32-bit
 // integer D: D format bits 4..5 = 2 (s32), A format 7..9 = 1 (s8), B format
@@ -97,35 +97,51 @@ __device__ __forceinline__ float gated(int act, float g, float u, float alpha, f
   return __fdividef(g, 1.f + __expf(-1.5957691216057308f * (g + 0.044715f * g * g * g))) * u;
 }
 
-// An epilogue warp's 128 weight columns of a tile: their scales lie in the 16
-// bytes that the rows of its staging block leave free (columns 4i .. 4i+3 in
-// row i), their biases behind the block.  Column 4i is `cols(i)` of the
-// expert's N columns; the loads are issued while the tile's product is still
-// running, since the scales come from HBM.
-constexpr int kWarpStage = kStageWarpBytes + 256;
-
-// First weight column of the warp's group i of four, or -1 past the end.
+// What one epilogue warp does of a tile: `n` output columns from column `col`
+// on, whose accumulators start at TMEM column `tcol` (concatenated: the up
+// columns BN / 2 further on), of the rows from row0 on that its lanes hold.  The
+// M = 64 accumulator holds row r in lane 32*(r/16) + r%16.
+struct Part {
+  int col, tcol;
+  int row0, lanes;  // rows row0 .. row0 + lanes - 1 of the tile
+};
 template <int MODE>
-__device__ __forceinline__ int group_col(const Int8Params& p, const TileCoord& tc, int part, int i) {
-  if constexpr (MODE == MODE_CONCAT) {  // 64 gate columns, then the 64 matching up columns
-    const int h = tc.n * 128 + part * 64 + 4 * (i & 15);
-    return h < p.out_cols ? (i >> 4) * p.out_cols + h : -1;
-  } else {
-    const int c = tc.n * BN + part * 128 + 4 * i;
-    return c < p.N ? c : -1;
-  }
+struct Cols {
+  static constexpr int OUT = MODE == MODE_DOWN ? BN : BN / 2;  // output columns of a tile
+  static constexpr int PER = BN / OUT;                         // accumulator columns per output column
+  static constexpr int n = OUT / 2;                            // output columns of a warp
+};
+
+template <int MODE>
+__device__ __forceinline__ Part warp_part(int tile_n, int quad, int part, bool half) {
+  using C = Cols<MODE>;
+  return {tile_n * C::OUT + part * C::n, MODE == MODE_CONCAT ? part * C::n : part * C::n * C::PER,
+          half ? quad * 16 : quad * 32, half ? 16 : 32};
 }
 
+// A warp's weight columns, in groups of four: group i's scales lie in the 16
+// bytes that row i of its staging block leaves free, its biases behind the
+// block.  The loads are issued while the tile's product is still running,
+// since the scales come from HBM.  Concatenated: the gate columns' groups,
+// then the up columns'.
+constexpr int kWarpStage = kStageWarpBytes + 256;
+
 template <int MODE>
-__device__ __forceinline__ void stage_columns(const Int8Params& p, const TileCoord& tc, int part, int lane,
-                                              uint8_t* stage) {
-  const int c = group_col<MODE>(p, tc, part, lane);
-  const int64_t base = static_cast<int64_t>(tc.e) * p.N;
+__device__ __forceinline__ void stage_columns(const Int8Params& p, const Part& w, int e, int lane, uint8_t* stage) {
+  int c = -1;  // the group's first weight column, or -1 past the end
+  if constexpr (MODE == MODE_CONCAT) {
+    const int h = w.col + 4 * (lane & 15);
+    if (h < p.out_cols) c = (lane < 16 ? 0 : p.out_cols) + h;
+  } else {
+    const int first = w.col * Cols<MODE>::PER + 4 * lane;
+    if (first < p.N) c = first;
+  }
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   uint2 b = make_uint2(0u, 0u);
   if (c >= 0) {
-    s = __ldg(reinterpret_cast<const float4*>(p.w_scales + base + c));
-    if (p.bias != nullptr) b = __ldg(reinterpret_cast<const uint2*>(p.bias + base + c));
+    const int64_t at = static_cast<int64_t>(e) * p.N + c;
+    s = __ldg(reinterpret_cast<const float4*>(p.w_scales + at));
+    if (p.bias != nullptr) b = __ldg(reinterpret_cast<const uint2*>(p.bias + at));
   }
   __syncwarp();  // every lane is done with the tile before
   *reinterpret_cast<float4*>(stage + lane * kStageRowBytes + 64) = s;
@@ -146,29 +162,31 @@ __device__ __forceinline__ float scaled(uint32_t acc, float row, const Col4& c, 
   return fmaf(static_cast<float>(static_cast<int>(acc)) * row, c.s[i], c.b[i]);
 }
 
-// 32 output columns of this thread's row, from column `rel` of the warp's part
-// of the tile (accumulator columns from tacc on), packed to bf16.
+// 32 output columns of this thread's row, from column `rel` of the warp's
+// columns, packed to bf16.
 template <int MODE>
-__device__ __forceinline__ void out_chunk(const Int8Params& p, uint32_t tacc, int part, int rel, float row,
+__device__ __forceinline__ void out_chunk(const Int8Params& p, const Part& w, uint32_t tacc, int rel, float row,
                                           const uint8_t* stage, uint32_t (&packed)[16]) {
+  const int i0 = rel >> 2;
   if constexpr (MODE == MODE_DOWN) {
     uint32_t a[32];
-    tmem_ld32(tacc + part * 128 + rel, a);
+    tmem_ld32(tacc + w.tcol + rel, a);
     tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-      const Col4 c = columns(stage, (rel + j) >> 2);
+      const Col4 c = columns(stage, i0 + (j >> 2));
       packed[j / 2] = pack_bf16x2(scaled(a[j], row, c, 0), scaled(a[j + 1], row, c, 1));
       packed[j / 2 + 1] = pack_bf16x2(scaled(a[j + 2], row, c, 2), scaled(a[j + 3], row, c, 3));
     }
   } else if constexpr (MODE == MODE_CONCAT) {
     uint32_t g[32], u[32];
-    tmem_ld32(tacc + part * 64 + rel, g);
-    tmem_ld32(tacc + 128 + part * 64 + rel, u);
+    tmem_ld32(tacc + w.tcol + rel, g);
+    tmem_ld32(tacc + w.tcol + BN / 2 + rel, u);
     tmem_ld_wait();
+    const int i1 = i0 + 16;
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-      const Col4 cg = columns(stage, (rel + j) >> 2), cu = columns(stage, 16 + ((rel + j) >> 2));
+      const Col4 cg = columns(stage, i0 + (j >> 2)), cu = columns(stage, i1 + (j >> 2));
       float h[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -178,12 +196,12 @@ __device__ __forceinline__ void out_chunk(const Int8Params& p, uint32_t tacc, in
     }
   } else {
     uint32_t a[64];
-    tmem_ld32(tacc + part * 128 + 2 * rel, a);
-    tmem_ld32(tacc + part * 128 + 2 * rel + 32, a + 32);
+    tmem_ld32(tacc + w.tcol + 2 * rel, a);
+    tmem_ld32(tacc + w.tcol + 2 * rel + 32, a + 32);
     tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 64; j += 4) {
-      const Col4 c = columns(stage, (2 * rel + j) >> 2);
+      const Col4 c = columns(stage, 2 * i0 + (j >> 2));
       const float h0 = gated(p.activation, scaled(a[j], row, c, 0), scaled(a[j + 1], row, c, 1), p.alpha, p.limit);
       const float h1 = gated(p.activation, scaled(a[j + 2], row, c, 2), scaled(a[j + 3], row, c, 3), p.alpha, p.limit);
       packed[j / 4] = pack_bf16x2(h0, h1);
@@ -191,36 +209,32 @@ __device__ __forceinline__ void out_chunk(const Int8Params& p, uint32_t tacc, in
   }
 }
 
-// One tile's epilogue for one warp (TMEM lane quadrant `quad`, half `part` of
-// the tile's output columns), rs its thread's row scale.  half: the M = 64
-// accumulator holds row r in lane 32*(r/16) + r%16.  Each 32 x 32 block is
-// turned through the staging block so that a store instruction writes 8 rows
+// One tile's epilogue for one warp, rs its thread's row scale; row0 the tile's
+// first row and rows how many there are.  Each 32 x 32 block is turned through the staging block so that a store instruction writes 8 rows
 // x 64 contiguous bytes.
 template <int MODE>
-__device__ __forceinline__ void epilogue(const Int8Params& p, const TileCoord& tc, uint32_t tacc, int quad, int part,
-                                         int lane, float rs, uint8_t* stage, bool half) {
-  constexpr int kPartCols = MODE == MODE_DOWN ? BN / 2 : BN / 4;  // output columns of the warp
-  const int col0 = tc.n * 2 * kPartCols + part * kPartCols;
+__device__ __forceinline__ void epilogue(const Int8Params& p, const Part& w, uint32_t tacc, int row0, int rows, int lane,
+                                         float rs, uint8_t* stage) {
   const int q = lane & 3;
   uint8_t* my_row = stage + lane * kStageRowBytes;
 #pragma unroll 1
-  for (int rel = 0; rel < kPartCols; rel += kOutChunk) {
-    if (col0 + rel >= p.out_cols) break;
+  for (int rel = 0; rel < Cols<MODE>::n; rel += kOutChunk) {
+    if (w.col + rel >= p.out_cols) break;
     uint32_t packed[16];
-    out_chunk<MODE>(p, tacc, part, rel, rs, stage, packed);
+    out_chunk<MODE>(p, w, tacc, rel, rs, stage, packed);
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       *reinterpret_cast<uint4*>(my_row + 16 * c) =
           make_uint4(packed[4 * c], packed[4 * c + 1], packed[4 * c + 2], packed[4 * c + 3]);
     __syncwarp();
-    const int col = col0 + rel + 8 * q;
+    const int col = w.col + rel + 8 * q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int l = 8 * i + (lane >> 2);  // the lane whose row this is
-      const int r = half ? quad * 16 + l : quad * 32 + l;
-      if ((!half || l < 16) && r < tc.rows && col < p.out_cols)
-        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(tc.row0) + r) * p.out_cols + col) =
+      const int r = w.row0 + l;
+      if (l < w.lanes && r < rows && col < p.out_cols)
+        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(row0) + r) * p.out_cols + col) =
             *reinterpret_cast<const uint4*>(stage + l * kStageRowBytes + 16 * q);
     }
   }
@@ -229,16 +243,17 @@ __device__ __forceinline__ void epilogue(const Int8Params& p, const TileCoord& t
 template <int MODE>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapAh,
-                     const __grid_constant__ CUtensorMap mapB, const Int8Params p) {
+                     const __grid_constant__ CUtensorMap mapAf, const __grid_constant__ CUtensorMap mapB,
+                     const Int8Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   uint8_t* ctrl = smem + STAGES * STAGE_BYTES;
-  const uint32_t full0 = smem_u32(ctrl);         // STAGES mbarriers
-  const uint32_t empty0 = full0 + 8 * STAGES;    // STAGES mbarriers
-  const uint32_t tfull0 = empty0 + 8 * STAGES;   // 2 mbarriers
-  const uint32_t tempty0 = tfull0 + 16;          // 2 mbarriers
-  const uint32_t drain_bar = tempty0 + 16;       // 1 mbarrier
+  const uint32_t full0 = smem_u32(ctrl);           // STAGES mbarriers
+  const uint32_t empty0 = full0 + 8 * STAGES;   // STAGES mbarriers
+  const uint32_t tfull0 = empty0 + 8 * STAGES;  // 2 mbarriers
+  const uint32_t tempty0 = tfull0 + 16;            // 2 mbarriers
+  const uint32_t drain_bar = tempty0 + 16;         // 1 mbarrier
   static_assert((2 * STAGES + 5) * 8 <= 128, "mbarriers overflow their part of the control block");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 128);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 132);
@@ -318,7 +333,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = true;
       for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
         const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
-        const bool half = tc.rows <= HALF_ROWS;
+        // rows of A to copy: all 128, or 64 of a tile of at most 64, or 16 of one
+        // of at most 16; the rest of the stage holds old rows, whose sums are
+        // not stored
+        const bool half = tc.rows <= HALF_ROWS, few = tc.rows <= FEW_ROWS;
+        const int a_rows = few ? FEW_ROWS : half ? HALF_ROWS : BM;
+        const CUtensorMap* ma = few ? &mapAf : half ? &mapAh : &mapA;
+        const uint32_t bytes = static_cast<uint32_t>(a_rows * BK + B_BYTES);
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t ph = static_cast<uint32_t>(it / STAGES) & 1u;
@@ -326,10 +347,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ok = false;
             break;
           }
-          const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + A_BYTES, fb = full0 + 8 * s;
-          mbar_arrive_expect_tx(fb, half ? HALF_A_BYTES + B_BYTES : STAGE_BYTES);
-          tma_load_2d(sa, half ? &mapAh : &mapA, fb, kb * BK, tc.row0);
-          if constexpr (MODE == MODE_CONCAT) tma_load_4d(sb, &mapB, fb, kb * BK, tc.n * 128, 0, tc.e);
+          const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + A_BYTES;
+          const uint32_t fb = full0 + 8 * s;
+          mbar_arrive_expect_tx(fb, bytes);
+          tma_load_2d(sa, ma, fb, kb * BK, tc.row0);
+          if constexpr (MODE == MODE_CONCAT) tma_load_4d(sb, &mapB, fb, kb * BK, tc.n * (BN / 2), 0, tc.e);
           else tma_load_3d(sb, &mapB, fb, kb * BK, tc.n * BN, tc.e);
         }
       }
@@ -379,8 +401,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int kk = 0; kk < BK / UMMA_K; ++kk) {
             // K-major rows of 128 B, 8-row swizzle atoms 1024 B apart; a
             // 32-wide K step is 32 B along the row
-            mma_i8_ss(d_tmem, smem_desc_sw128(sa + kk * UMMA_K, 16, 1024),
-                      smem_desc_sw128(sb + kk * UMMA_K, 16, 1024), idesc, (kb | kk) != 0 ? 1u : 0u);
+            const uint64_t da = smem_desc_sw128(sa + kk * UMMA_K, 16, 1024), db = smem_desc_sw128(sb + kk * UMMA_K, 16, 1024);
+            mma_i8_ss(d_tmem, da, db, idesc, (kb | kk) != 0 ? 1u : 0u);
           }
           mma_commit(empty0 + 8 * s);
         }
@@ -402,15 +424,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
       const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
       const int acc = ti & 1;
-      const bool half = tc.rows <= HALF_ROWS;
-      const int row = half ? quad * 16 + lane : quad * 32 + lane;
-      const float rs = (!half || lane < 16) && row < tc.rows ? __ldg(p.a_scales + tc.row0 + row) : 0.f;
-      stage_columns<MODE>(p, tc, part, lane, stage);
+      const Part w = warp_part<MODE>(tc.n, quad, part, tc.rows <= HALF_ROWS);
+      const float rs = lane < w.lanes && w.row0 + lane < tc.rows ? __ldg(p.a_scales + tc.row0 + w.row0 + lane) : 0.f;
+      stage_columns<MODE>(p, w, tc.e, lane, stage);
       const bool got = mbar_wait(tfull0 + 8 * acc, static_cast<uint32_t>(ti >> 1) & 1u, abort_flag, kTimeoutNs);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after_sync();
       const uint32_t tacc = tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quad * 32) << 16);
-      epilogue<MODE>(p, tc, tacc, quad, part, lane, rs, stage, half);
+      epilogue<MODE>(p, w, tacc, tc.row0, tc.rows, lane, rs, stage);
       tc_fence_before_sync();
       mbar_arrive(tempty0 + 8 * acc);
     }
@@ -427,8 +448,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 constexpr size_t smem_bytes(int E) {
-  return 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + CTRL_BYTES + 2 * static_cast<size_t>(E + 1) * 4 + 16 +
-         NUM_EPI_WARPS * kWarpStage;
+  return 1024 + STAGES * STAGE_BYTES + CTRL_BYTES + 2 * static_cast<size_t>(E + 1) * 4 + 16 + NUM_EPI_WARPS * kWarpStage;
 }
 
 template <int MODE>
@@ -438,16 +458,18 @@ cudaError_t launch_mode(const Int8GemmArgs& a, cudaStream_t stream) {
   const cuuint64_t pitch = static_cast<cuuint64_t>(int8_pitch(K));
   const cuuint64_t N = down ? a.H : 2 * static_cast<cuuint64_t>(a.D), E = a.E;
   constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  CUtensorMap mapA, mapAh, mapB;
+  CUtensorMap mapA, mapAh, mapAf, mapB;
   {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(a.R)};
     const cuuint64_t strides[1] = {pitch};
-    const cuuint32_t box[2] = {BK, BM}, half_box[2] = {BK, HALF_ROWS};
-    if (!encode_tiled_map(&mapA, kU8, a.A, 2, dims, strides, box)) return cudaErrorInvalidValue;
-    if (!encode_tiled_map(&mapAh, kU8, a.A, 2, dims, strides, half_box)) return cudaErrorInvalidValue;
+    const cuuint32_t box[2] = {BK, BM}, half_box[2] = {BK, HALF_ROWS}, few_box[2] = {BK, FEW_ROWS};
+    if (!encode_tiled_map(&mapA, kU8, a.A, 2, dims, strides, box) ||
+        !encode_tiled_map(&mapAh, kU8, a.A, 2, dims, strides, half_box) ||
+        !encode_tiled_map(&mapAf, kU8, a.A, 2, dims, strides, few_box))
+      return cudaErrorInvalidValue;
   }
   if (MODE == MODE_CONCAT) {
-    // {K, D, 2 (gate/up), E}: 128 gate rows, then the 128 matching up rows
+    // {K, D, 2 (gate/up), E}: a CTA's gate rows, then the matching up rows
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(a.D), 2, E};
     const cuuint64_t strides[3] = {pitch, a.D * pitch, N * pitch};
     const cuuint32_t box[4] = {BK, BN / 2, 2, 1};
@@ -469,18 +491,19 @@ cudaError_t launch_mode(const Int8GemmArgs& a, cudaStream_t stream) {
   p.R = a.R;
   p.N = static_cast<int>(N);
   p.out_cols = down ? a.H : a.D;
-  p.n_tiles = down ? (a.H + BN - 1) / BN : (a.D + 127) / 128;
+  p.n_tiles = (p.out_cols + (down ? BN : BN / 2) - 1) / (down ? BN : BN / 2);
   p.num_kb = (K + BK - 1) / BK;
   p.activation = a.activation;
   p.alpha = a.alpha;
   p.limit = a.limit;
   p.err_bit = down ? MOE_DEVICE_ERR_TIMEOUT_GEMM2 : MOE_DEVICE_ERR_TIMEOUT_GEMM1;
-  const cudaError_t err = opt_in_dynamic_smem(reinterpret_cast<const void*>(int8_gemm_kernel<MODE>),
-                                              static_cast<int>(smem_bytes(kMaxExperts)));
+  const void* kernel = reinterpret_cast<const void*>(int8_gemm_kernel<MODE>);
+  const cudaError_t err = opt_in_dynamic_smem(kernel, static_cast<int>(smem_bytes(kMaxExperts)));
   if (err != cudaSuccess) return err;
   const int64_t max_tiles = (static_cast<int64_t>(a.R) / BM + std::min(a.E, a.R)) * p.n_tiles;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(max_tiles, a.num_sms)));
-  return launch_pdl(int8_gemm_kernel<MODE>, grid, dim3(NUM_THREADS), smem_bytes(a.E), stream, mapA, mapAh, mapB, p);
+  return launch_pdl(int8_gemm_kernel<MODE>, grid, dim3(NUM_THREADS), smem_bytes(a.E), stream, mapA, mapAh, mapAf, mapB,
+                    p);
 }
 
 }  // namespace
