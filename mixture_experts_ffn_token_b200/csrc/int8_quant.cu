@@ -56,11 +56,11 @@ __device__ __forceinline__ uint2 quant8(const uint4& u, const Quant& q) {
 
 // 2^g_log threads per row (a warp at least, 256 / 2^g_log rows a block), 16
 // values a thread and step; the row stays in registers between the maximum
-// and the rounding (up to kHeld steps), so it is read once and its k copies
+// and the rounding (up to HELD steps), so it is read once and its k copies
 // are written once each.
-constexpr int kHeld = 2;
 constexpr int kQuantThreads = 512;
 
+template <int HELD>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv_bfloat16* __restrict__ in, int rows,
                                                                       int n, int g_log,
                                                                       const int32_t* __restrict__ inverse, int k,
@@ -75,17 +75,17 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv
   const int chunks = (n + 15) / 16, vec = live ? n / 8 : 0;  // nothing is read of a row that is not live
   const uint4* src = reinterpret_cast<const uint4*>(in + row * n);
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 a[kHeld], b[kHeld];
+  uint4 a[HELD], b[HELD];
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
+  for (int i = 0; i < HELD; ++i) {
     const int c = tid + i * steps;
     a[i] = 2 * c < vec ? __ldg(src + 2 * c) : zero;
     b[i] = 2 * c + 1 < vec ? __ldg(src + 2 * c + 1) : zero;
   }
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) m = absmax8(absmax8(m, a[i]), b[i]);
-  for (int c = tid + kHeld * steps; 2 * c < vec; c += steps) {
+  for (int i = 0; i < HELD; ++i) m = absmax8(absmax8(m, a[i]), b[i]);
+  for (int c = tid + HELD * steps; 2 * c < vec; c += steps) {
     m = absmax8(m, __ldg(src + 2 * c));
     if (2 * c + 1 < vec) m = absmax8(m, __ldg(src + 2 * c + 1));
   }
@@ -110,11 +110,11 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv
     }
   };
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
+  for (int i = 0; i < HELD; ++i) {
     const int c = tid + i * steps;
     if (c < chunks) store(c, a[i], b[i]);
   }
-  for (int c = tid + kHeld * steps; c < chunks; c += steps)
+  for (int c = tid + HELD * steps; c < chunks; c += steps)
     store(c, __ldg(src + 2 * c), 2 * c + 1 < vec ? __ldg(src + 2 * c + 1) : zero);
   for (int j = tid; j < k; j += steps) {
     const int64_t p = inverse != nullptr ? inverse[row * k + j] : row;
@@ -204,19 +204,30 @@ __global__ void __launch_bounds__(kWThreads) quantize_weights_kernel(const __nv_
   }
 }
 
-}  // namespace
-
-cudaError_t launch_quantize_rows(const __nv_bfloat16* in, int rows, int n, const int32_t* inverse, int k, int R,
-                                 const int32_t* total, int8_t* q, float* scales, cudaStream_t stream) {
-  if (rows == 0) return cudaSuccess;
+template <int HELD>
+cudaError_t launch_rows(const __nv_bfloat16* in, int rows, int n, const int32_t* inverse, int k, int R,
+                        const int32_t* total, int8_t* q, float* scales, cudaStream_t stream) {
   // as many threads as hold the row in registers
   const int chunks = (n + 15) / 16;
   int g_log = 5;
-  while ((1 << g_log) * kHeld < chunks && (1 << g_log) < kQuantThreads) ++g_log;
+  while ((HELD << g_log) < chunks && (1 << g_log) < kQuantThreads) ++g_log;
   const int threads = std::max(256, 1 << g_log), per_block = threads >> g_log;
-  return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)),
+  return launch_pdl(quantize_rows_kernel<HELD>, dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)),
                     dim3(static_cast<unsigned>(threads)), 0, stream, in, rows, n, g_log, inverse, k, R, total, q,
                     scales);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const __nv_bfloat16* in, int rows, int n, const int32_t* inverse, int k, int R,
+                                 const int32_t* total, int8_t* q, float* scales, int num_sms, cudaStream_t stream) {
+  if (rows == 0) return cudaSuccess;
+  // Four steps a thread keep most in flight (8192 rows of 14336: 70.3 us with two, 56.7 with four; of 2880: 17.6,
+  // 15.4), two where a warp then holds a short row (49152 of 768: 24.6 us, 29.8 with four), and with few rows one,
+  // for the shortest way through (32 rows of 4096 to 8 places: 2.4 us, 3.4 with two, 4.6 with four).
+  if (rows <= 2 * num_sms) return launch_rows<1>(in, rows, n, inverse, k, R, total, q, scales, stream);
+  if (n <= 1024) return launch_rows<2>(in, rows, n, inverse, k, R, total, q, scales, stream);
+  return launch_rows<4>(in, rows, n, inverse, k, R, total, q, scales, stream);
 }
 
 cudaError_t launch_quantize_weights(const __nv_bfloat16* w, int E, int K, int N, int8_t* q, float* scales,

@@ -224,7 +224,7 @@ inline int int8_pitch(int n) { return (n + 15) / 16 * 16; }
 // for the k positions p of every row (inverse, may be null: p = the row).
 // total (may be null): device int, rows from it on are left alone.
 cudaError_t launch_quantize_rows(const __nv_bfloat16* in, int rows, int n, const int32_t* inverse, int k, int R,
-                                 const int32_t* total, int8_t* q, float* scales, cudaStream_t stream);
+                                 const int32_t* total, int8_t* q, float* scales, int num_sms, cudaStream_t stream);
 // W [E,K,N] bf16 -> q [E,N,int8_pitch(K)], scales [E,N] (per column).
 cudaError_t launch_quantize_weights(const __nv_bfloat16* w, int E, int K, int N, int8_t* q, float* scales,
                                     cudaStream_t stream);

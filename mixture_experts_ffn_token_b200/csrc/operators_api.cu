@@ -206,7 +206,7 @@ moe_status_t moe_dispatch_int8(const moe_config_t* cfg, const void* x, const int
   if ((st = current_device(&num_sms)) != MOE_OK) return st;
   return cuda_status(moe::launch_quantize_rows(static_cast<const __nv_bfloat16*>(x), cfg->num_tokens, cfg->hidden_dim,
                                                inverse, cfg->top_k, cfg->num_tokens * cfg->top_k, nullptr, rows_q,
-                                               row_scales, reinterpret_cast<cudaStream_t>(stream)));
+                                               row_scales, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_quantize_rows(const moe_config_t* cfg, const void* h, const int32_t* expert_offsets, int8_t* rows_q,
@@ -222,7 +222,7 @@ moe_status_t moe_quantize_rows(const moe_config_t* cfg, const void* h, const int
   const int R = cfg->num_tokens * cfg->top_k;
   return cuda_status(moe::launch_quantize_rows(
       static_cast<const __nv_bfloat16*>(h), R, cfg->moe_dim, nullptr, 1, R,
-      expert_offsets != nullptr ? expert_offsets + cfg->num_experts : nullptr, rows_q, row_scales,
+      expert_offsets != nullptr ? expert_offsets + cfg->num_experts : nullptr, rows_q, row_scales, num_sms,
       reinterpret_cast<cudaStream_t>(stream)));
 }
 

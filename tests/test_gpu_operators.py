@@ -257,7 +257,8 @@ def test_router_gradient_against_differences(sink):
 
 
 # ------------------------------------------------------------------ 8-bit
-QUANT = [(1, 8, 1), (3, 24, 2), (5, 520, 3), (2, 4096, 8), (7, 16400, 2), (4, 2880, 1)]
+QUANT = [(1, 8, 1), (3, 24, 2), (5, 520, 3), (2, 4096, 8), (7, 16400, 2), (4, 2880, 1), (600, 1000, 2), (450, 2888, 4),
+         (333, 33000, 1)]
 
 
 @pytest.mark.parametrize("T,H,k", QUANT)
@@ -286,7 +287,7 @@ def test_dispatch_int8(T, H, k):
     assert torch.equal(s.cpu(), want_s)
 
 
-@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("rows", [1, 70, 400])
 @pytest.mark.parametrize("n", [8, 264, 1536, 33000])
 def test_quantize_rows(rows, n):
     cfg = abi.config(rows, 8, 3, 1, n)
