@@ -379,11 +379,24 @@ def _take(device, name, t, dtype, numel, required=True):
     raise ValueError(f"{name} must be dense (contiguous)")
 
 
+_cuda_in_use = False
+
+
 def _device() -> int:
-    # (once CUDA is in use, the first test is all)
-    if torch.cuda.is_initialized() or torch.cuda.is_available():
-        return torch.cuda.current_device()
-    return -1
+    """The current CUDA device (-1: this machine has none)."""
+    global _cuda_in_use
+    if _cuda_in_use:
+        return torch._C._cuda_getDevice()
+    if not torch.cuda.is_available():
+        return -1
+    dev = torch.cuda.current_device()
+    _cuda_in_use = True
+    return dev
+
+
+def _on(device, stream):
+    """The handle of `stream`, or of the current stream of `device`."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _rows_dtype(name, t):
@@ -410,37 +423,40 @@ def moe_dispatch(cfg, x, inverse, rows, expert_weights=None, stream=None):
     """rows[inverse[t*k+j]] = expert_weights[t, j] * x[t]: tokens [T, H] (bf16
     or fp32) to rows sorted by expert [T*k, H]."""
     dt, dev = _rows_dtype("x", x), _device()
-    T, H, R = cfg.num_tokens, cfg.hidden_dim, cfg.num_tokens * cfg.top_k
+    T, H = cfg.num_tokens, cfg.hidden_dim
+    R = T * cfg.top_k
     _check(load_library().moe_dispatch(
         ctypes.byref(cfg), dt, _take(dev, "x", x, x.dtype, T * H), _take(dev, "inverse", inverse, torch.int32, R),
         _take(dev, "expert_weights", expert_weights, torch.float32, R, False),
-        _take(dev, "rows", rows, x.dtype, R * H), _stream(stream)), "moe_dispatch")
+        _take(dev, "rows", rows, x.dtype, R * H), _on(dev, stream)), "moe_dispatch")
 
 
 def moe_dispatch_backward(cfg, d_rows, inverse, d_x, x=None, expert_weights=None, d_expert_weights=None, stream=None):
     """d_x[t] = sum_j expert_weights[t, j] * d_rows[inverse[t*k+j]] and, given x,
     d_expert_weights[t, j] = <x[t], d_rows[inverse[t*k+j]]>."""
     dt, dev = _rows_dtype("d_rows", d_rows), _device()
-    T, H, R = cfg.num_tokens, cfg.hidden_dim, cfg.num_tokens * cfg.top_k
+    T, H = cfg.num_tokens, cfg.hidden_dim
+    R = T * cfg.top_k
     _check(load_library().moe_dispatch_backward(
         ctypes.byref(cfg), dt, _take(dev, "d_rows", d_rows, d_rows.dtype, R * H),
         _take(dev, "x", x, d_rows.dtype, T * H, d_expert_weights is not None),
         _take(dev, "inverse", inverse, torch.int32, R),
         _take(dev, "expert_weights", expert_weights, torch.float32, R, False),
         _take(dev, "d_x", d_x, d_rows.dtype, T * H),
-        _take(dev, "d_expert_weights", d_expert_weights, torch.float32, R, False), _stream(stream)),
+        _take(dev, "d_expert_weights", d_expert_weights, torch.float32, R, False), _on(dev, stream)),
         "moe_dispatch_backward")
 
 
 def moe_combine(cfg, rows, inverse, out, expert_weights=None, stream=None):
     """out[t] = sum_j expert_weights[t, j] * rows[inverse[t*k+j]]."""
     dt, dev = _rows_dtype("rows", rows), _device()
-    T, H, R = cfg.num_tokens, cfg.hidden_dim, cfg.num_tokens * cfg.top_k
+    T, H = cfg.num_tokens, cfg.hidden_dim
+    R = T * cfg.top_k
     _check(load_library().moe_combine(
         ctypes.byref(cfg), dt, _take(dev, "rows", rows, rows.dtype, R * H),
         _take(dev, "inverse", inverse, torch.int32, R),
         _take(dev, "expert_weights", expert_weights, torch.float32, R, False),
-        _take(dev, "out", out, rows.dtype, T * H), _stream(stream)), "moe_combine")
+        _take(dev, "out", out, rows.dtype, T * H), _on(dev, stream)), "moe_combine")
 
 
 def moe_combine_backward(cfg, d_out, inverse, d_rows, rows=None, expert_weights=None, d_expert_weights=None,
@@ -448,14 +464,15 @@ def moe_combine_backward(cfg, d_out, inverse, d_rows, rows=None, expert_weights=
     """d_rows[inverse[t*k+j]] = expert_weights[t, j] * d_out[t] and, given rows,
     d_expert_weights[t, j] = <d_out[t], rows[inverse[t*k+j]]>."""
     dt, dev = _rows_dtype("d_out", d_out), _device()
-    T, H, R = cfg.num_tokens, cfg.hidden_dim, cfg.num_tokens * cfg.top_k
+    T, H = cfg.num_tokens, cfg.hidden_dim
+    R = T * cfg.top_k
     _check(load_library().moe_combine_backward(
         ctypes.byref(cfg), dt, _take(dev, "d_out", d_out, d_out.dtype, T * H),
         _take(dev, "rows", rows, d_out.dtype, R * H, d_expert_weights is not None),
         _take(dev, "inverse", inverse, torch.int32, R),
         _take(dev, "expert_weights", expert_weights, torch.float32, R, False),
         _take(dev, "d_rows", d_rows, d_out.dtype, R * H),
-        _take(dev, "d_expert_weights", d_expert_weights, torch.float32, R, False), _stream(stream)),
+        _take(dev, "d_expert_weights", d_expert_weights, torch.float32, R, False), _on(dev, stream)),
         "moe_combine_backward")
 
 
@@ -478,17 +495,18 @@ def moe_route_backward(cfg, logits, expert_indices, d_expert_weights, d_logits, 
         _take(dev, "d_sink_weights", d_sink_weights, torch.float32, T * S, False),
         _take(dev, "d_logits", d_logits, dt, n),
         _take(dev, "d_global_scale", d_global_scale, torch.float32, 1, False), ws,
-        0 if workspace is None else workspace.numel(), _stream(stream)), "moe_route_backward")
+        0 if workspace is None else workspace.numel(), _on(dev, stream)), "moe_route_backward")
 
 
 def moe_dispatch_int8(cfg, x, inverse, rows_q, row_scales, stream=None):
     """moe_dispatch of bf16 tokens to 8-bit rows [T*k, int8_pitch(H)] and their scales [T*k]."""
     dev = _device()
-    T, H, R = cfg.num_tokens, cfg.hidden_dim, cfg.num_tokens * cfg.top_k
+    T, H = cfg.num_tokens, cfg.hidden_dim
+    R = T * cfg.top_k
     _check(load_library().moe_dispatch_int8(
         ctypes.byref(cfg), _take(dev, "x", x, torch.bfloat16, T * H), _take(dev, "inverse", inverse, torch.int32, R),
         _take(dev, "rows_q", rows_q, torch.int8, R * int8_pitch(H)),
-        _take(dev, "row_scales", row_scales, torch.float32, R), _stream(stream)), "moe_dispatch_int8")
+        _take(dev, "row_scales", row_scales, torch.float32, R), _on(dev, stream)), "moe_dispatch_int8")
 
 
 def moe_quantize_rows(cfg, h, expert_offsets, rows_q, row_scales, stream=None):
@@ -500,7 +518,7 @@ def moe_quantize_rows(cfg, h, expert_offsets, rows_q, row_scales, stream=None):
         ctypes.byref(cfg), _take(dev, "h", h, torch.bfloat16, R * D),
         _take(dev, "expert_offsets", expert_offsets, torch.int32, cfg.num_experts + 1, False),
         _take(dev, "rows_q", rows_q, torch.int8, R * int8_pitch(D)),
-        _take(dev, "row_scales", row_scales, torch.float32, R), _stream(stream)), "moe_quantize_rows")
+        _take(dev, "row_scales", row_scales, torch.float32, R), _on(dev, stream)), "moe_quantize_rows")
 
 
 def _contraction(cfg, which):
@@ -519,7 +537,7 @@ def moe_quantize_weights(cfg, contraction, w, w_q, w_scales, stream=None):
     _check(load_library().moe_quantize_weights(
         ctypes.byref(cfg), which, _take(dev, "w", w, torch.bfloat16, E * K * N),
         _take(dev, "w_q", w_q, torch.int8, E * N * int8_pitch(K)),
-        _take(dev, "w_scales", w_scales, torch.float32, E * N), _stream(stream)), "moe_quantize_weights")
+        _take(dev, "w_scales", w_scales, torch.float32, E * N), _on(dev, stream)), "moe_quantize_weights")
 
 
 def moe_grouped_linear_int8(cfg, contraction, rows_q, row_scales, w_q, w_scales, expert_offsets, out, workspace,
@@ -537,4 +555,4 @@ def moe_grouped_linear_int8(cfg, contraction, rows_q, row_scales, w_q, w_scales,
         _take(dev, "expert_offsets", expert_offsets, torch.int32, E + 1),
         _take(dev, "out", out, torch.bfloat16, R * (cfg.hidden_dim if which else cfg.moe_dim)),
         _take(dev, "workspace", workspace, torch.uint8, workspace.numel() if workspace is not None else 0),
-        workspace.numel(), _stream(stream)), "moe_grouped_linear_int8")
+        workspace.numel(), _on(dev, stream)), "moe_grouped_linear_int8")

@@ -24,7 +24,7 @@ void refresh_switches() {
   constexpr size_t kPrefixLen = sizeof(kPrefix) - 1;
   for (char** e = environ; e != nullptr && *e != nullptr; ++e) {
     const char* kv = *e;
-    if (std::strncmp(kv, kPrefix, kPrefixLen) != 0) continue;
+    if (kv[0] != kPrefix[0] || std::strncmp(kv, kPrefix, kPrefixLen) != 0) continue;
     const char* name = kv + kPrefixLen;
     const char* eq = std::strchr(name, '=');
     if (eq == nullptr) continue;

@@ -333,7 +333,7 @@ def test_rows_with_nan_or_infinity_get_nan_scales():
 
 
 @pytest.mark.parametrize("part", ["gate_up", "down"])
-@pytest.mark.parametrize("E,H,D", [(1, 8, 8), (3, 264, 40), (2, 136, 520), (1, 1000, 72)])
+@pytest.mark.parametrize("E,H,D", [(1, 8, 8), (3, 264, 40), (2, 136, 520), (1, 1000, 72), (1, 4104, 24), (1, 16, 12304), (2, 40, 1288)])
 def test_quantize_weights(E, H, D, part):
     cfg = abi.config(2, H, E, 1, D)
     K, N = (H, 2 * D) if part == "gate_up" else (D, H)
