@@ -20,6 +20,8 @@ namespace moe {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kGatherLog = 7;
+constexpr int kGatherThreads = 1 << kGatherLog;  // (2 to 4% less time than 256: the last wave is finer)
 
 // 16 bytes of a row: 8 bf16 or 4 fp32 values.
 template <bool F32>
@@ -51,7 +53,7 @@ struct Vec {
   }
 };
 
-// A block covers u * 2^cw_log columns (16-byte vectors) of 256 / 2^cw_log tokens.
+// A block covers u * 2^cw_log columns (16-byte vectors) of blockDim / 2^cw_log tokens.
 struct Tiling {
   int cw_log, chunks;
 };
@@ -113,13 +115,13 @@ __global__ void __launch_bounds__(kRowThreads) spread_kernel(const RowsArgs a, i
 // out[t] = sum_j w * rows[p], j ascending in fp32.  A thread loads U columns of
 // up to KB rows before it adds the first.
 template <bool F32, int KB, int U>
-__global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsArgs a, int cw_log, int chunks) {
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const RowsArgs a, int cw_log, int chunks) {
   griddep_wait();  // the previous kernel's results are complete and visible
   griddep_launch_dependents();
   const uint32_t tile = blockIdx.x / static_cast<uint32_t>(chunks);
   const int cw = 1 << cw_log;
   const int c0 = static_cast<int>((blockIdx.x - tile * chunks) * U) * cw + (threadIdx.x & (cw - 1));
-  const int64_t t = (static_cast<int64_t>(tile) << (8 - cw_log)) + (threadIdx.x >> cw_log);
+  const int64_t t = (static_cast<int64_t>(tile) << (kGatherLog - cw_log)) + (threadIdx.x >> cw_log);
   if (t >= a.T || c0 >= a.vec) return;
   const uint4* rows = static_cast<const uint4*>(a.rows_in) + c0;
   Vec<F32> acc[U];
@@ -460,10 +462,11 @@ cudaError_t launch_dot(const RowsArgs& a, cudaStream_t stream) {
 template <bool F32, int KB, int U>
 cudaError_t launch_copy(const RowsArgs& a, bool spread, cudaStream_t stream) {
   const Tiling tl = tiling(a.vec, spread ? 1 : U);
-  const int per_block = kRowThreads >> tl.cw_log;
+  const int threads = spread ? kRowThreads : kGatherThreads;
+  const int per_block = threads >> tl.cw_log;
   const int64_t blocks = (static_cast<int64_t>(a.T) + per_block - 1) / per_block * tl.chunks;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(kRowThreads);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(static_cast<unsigned>(threads));
   if (spread) return launch_pdl(spread_kernel<F32, KB>, grid, block, 0, stream, a, tl.cw_log, tl.chunks);
   return launch_pdl(gather_kernel<F32, KB, U>, grid, block, 0, stream, a, tl.cw_log, tl.chunks);
 }
