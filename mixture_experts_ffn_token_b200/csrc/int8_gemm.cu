@@ -89,8 +89,9 @@ struct Int8Params {
 // the quotient is 0, as the limit is.
 __device__ __forceinline__ float gated(int act, float g, float u, float alpha, float limit) {
   if (act != 2 && limit > 0.f) {
-    g = fminf(g, limit);
-    u = fminf(fmaxf(u, -limit), limit);
+    // (comparisons, so that a NaN stays one)
+    g = g > limit ? limit : g;
+    u = u > limit ? limit : u < -limit ? -limit : u;
   }
   if (act == 0) return __fdividef(g, 1.f + __expf(-g)) * u;
   if (act == 1) return __fdividef(g, 1.f + __expf(-alpha * g)) * (u + 1.f);

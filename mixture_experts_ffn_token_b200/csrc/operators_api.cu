@@ -22,8 +22,7 @@ moe_status_t check_operator_workspace(const void* ws, size_t bytes) {
   return bytes < kOperatorWorkspace ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
-// What the four row operators check alike.  a, b: the token-side and the
-// sorted-side tensor (b may be null where it is not needed).
+// What the four row operators check alike.
 moe_status_t check_rows(const moe_config_t* cfg, moe_dtype_t dtype, const int32_t* inverse) {
   const moe_status_t st = validate_config(cfg);
   if (st != MOE_OK) return st;
@@ -87,7 +86,7 @@ moe_status_t moe_dispatch(const moe_config_t* cfg, moe_dtype_t dtype, const void
   moe_status_t st = check_rows(cfg, dtype, inverse);
   if (st != MOE_OK) return st;
   if (cfg->num_tokens == 0) return MOE_OK;
-  if (!given(x) || !given(rows)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!given(x) || !given(rows) || x == rows) return MOE_ERR_INVALID_ARGUMENT;
   int num_sms = 0;
   if ((st = current_device(&num_sms)) != MOE_OK) return st;
   moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights, num_sms);
@@ -106,6 +105,7 @@ moe_status_t moe_dispatch_backward(const moe_config_t* cfg, moe_dtype_t dtype, c
   if (cfg->num_tokens == 0) return MOE_OK;
   if (!given(d_rows) || !given(d_x) || !given_or_null(x)) return MOE_ERR_INVALID_ARGUMENT;
   if (d_expert_weights != nullptr && x == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (d_x == x || d_x == d_rows) return MOE_ERR_INVALID_ARGUMENT;  // not in place
   int num_sms = 0;
   if ((st = current_device(&num_sms)) != MOE_OK) return st;
   moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights, num_sms);
@@ -123,7 +123,7 @@ moe_status_t moe_combine(const moe_config_t* cfg, moe_dtype_t dtype, const void*
   moe_status_t st = check_rows(cfg, dtype, inverse);
   if (st != MOE_OK) return st;
   if (cfg->num_tokens == 0) return MOE_OK;
-  if (!given(rows) || !given(out)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!given(rows) || !given(out) || rows == out) return MOE_ERR_INVALID_ARGUMENT;
   int num_sms = 0;
   if ((st = current_device(&num_sms)) != MOE_OK) return st;
   moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights, num_sms);
@@ -142,6 +142,7 @@ moe_status_t moe_combine_backward(const moe_config_t* cfg, moe_dtype_t dtype, co
   if (cfg->num_tokens == 0) return MOE_OK;
   if (!given(d_out) || !given(d_rows) || !given_or_null(rows)) return MOE_ERR_INVALID_ARGUMENT;
   if (d_expert_weights != nullptr && rows == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (d_rows == rows || d_rows == d_out) return MOE_ERR_INVALID_ARGUMENT;  // not in place
   int num_sms = 0;
   if ((st = current_device(&num_sms)) != MOE_OK) return st;
   moe::RowsArgs a = rows_args(cfg, dtype, inverse, expert_weights, num_sms);
@@ -168,7 +169,7 @@ moe_status_t moe_route_backward(const moe_config_t* cfg, const void* logits, con
     if ((st = check_operator_workspace(workspace, workspace_bytes)) != MOE_OK) return st;
   }
   if (cfg->num_tokens > 0 && (logits == nullptr || expert_indices == nullptr || d_expert_weights == nullptr ||
-                              d_logits == nullptr))
+                              d_logits == nullptr || d_logits == logits))
     return MOE_ERR_INVALID_ARGUMENT;
   if (cfg->num_tokens == 0 && d_global_scale == nullptr) return MOE_OK;
   int num_sms = 0;

@@ -256,6 +256,90 @@ def test_router_gradient_against_differences(sink):
             assert abs((loss(up) - loss(down)) / (2 * h) - float(got[t, c])) <= worst * h * h / 6 + 1e-6
 
 
+def test_no_tokens():
+    """A batch of no tokens enqueues nothing; the global scale's gradient is the empty sum."""
+    E, S, k = 4, 1, 3
+    cfg = abi.config(0, 64, E, k, 64, router="sigmoid_sink", num_sink=S)
+    ws = torch.full((abi.moe_operator_workspace_size(cfg),), 255, dtype=torch.uint8, device="cuda")
+    e = lambda *s, dtype=F32: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+    i32, i8 = torch.int32, torch.int8
+    d_gs = torch.full((1,), 7.0, device="cuda")
+    abi.moe_route_backward(cfg, e(0, E + S), e(0, k, dtype=i32), e(0, k), e(0, E + S), d_sink_weights=e(0, S),
+                           d_global_scale=d_gs, workspace=ws)
+    assert float(d_gs) == 0.0
+    abi.moe_dispatch(cfg, e(0, 64), e(0, dtype=i32), e(0, 64))
+    abi.moe_combine_backward(cfg, e(0, 64), e(0, dtype=i32), e(0, 64), rows=e(0, 64), d_expert_weights=e(0, k))
+    abi.moe_dispatch_int8(cfg, e(0, 64, dtype=BF16), e(0, dtype=i32), e(0, 64, dtype=i8), e(0))
+    abi.moe_quantize_rows(cfg, e(0, 64, dtype=BF16), None, e(0, 64, dtype=i8), e(0))
+    abi.moe_grouped_linear_int8(cfg, "down", e(0, 64, dtype=i8), e(0), e(E, 64, 64, dtype=i8), e(E, 64),
+                                torch.zeros(E + 1, dtype=i32, device="cuda"), e(0, 64, dtype=BF16), ws)
+    torch.cuda.synchronize()
+
+
+def test_rows_past_32_bits():
+    """Rows whose offsets pass 2^32 bytes and 2^31 values, in every row operator."""
+    T, H, E, k = 140000, 8192, 4, 2
+    cfg = abi.config(T, H, E, k, 8)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, H, generator=g, device="cuda", dtype=BF16)
+    inv = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    rows, out, d_w = torch.zeros(T * k, H, dtype=BF16, device="cuda"), torch.zeros_like(x), torch.zeros(T, k, device="cuda")
+    abi.moe_dispatch(cfg, x, inv, rows, expert_weights=w)
+    p2 = inv.view(T, k).long()
+    some = torch.cat([torch.arange(50), torch.arange(T - 50, T)]).cuda()
+    ref = (w[some][:, :, None].double() * x[some][:, None].double())
+    assert ((rows[p2[some]].double() - ref).abs() <= ref.abs() * (R.HALF[BF16] + 2 * R.F32)).all()
+    assert T * k * H > 2 ** 31 and int(p2[some].max()) * H > 2 ** 31
+    terms = w[some][:, :, None].double() * rows[p2[some]].double()
+    ref, mag = terms.sum(1), terms.abs().sum(1)
+    dot = (x[some][:, None].double() * rows[p2[some]].double())
+    for grad in (False, True):
+        if grad:
+            abi.moe_dispatch_backward(cfg, rows, inv, out, x=x, expert_weights=w, d_expert_weights=d_w)
+            assert ((d_w[some].double() - dot.sum(2)).abs() <= R.tol_dots(dot.abs().sum(2), H)).all()
+        else:
+            abi.moe_combine(cfg, rows, inv, out, expert_weights=w)
+        assert ((out[some].double() - ref).abs() <= R.tol_gather(ref, mag, k, BF16)).all()
+    d_rows = torch.zeros_like(rows)
+    abi.moe_combine_backward(cfg, x, inv, d_rows, rows=rows, expert_weights=w, d_expert_weights=d_w)
+    assert torch.equal(d_rows, rows)                       # the same products as the dispatch's
+    assert ((d_w[some].double() - dot.sum(2)).abs() <= R.tol_dots(dot.abs().sum(2), H)).all()
+
+
+def test_int8_past_32_bits():
+    """8-bit rows and weights past 2^31 bytes, a product past 2^31 values."""
+    T, H, D, E = 270000, 8192, 8200, 16
+    cfg = abi.config(T, H, E, 1, D)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, H, generator=g, device="cuda", dtype=BF16)
+    inv = torch.randperm(T, generator=g, device="cuda").to(torch.int32)
+    q, s = torch.empty(T, H, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    abi.moe_dispatch_int8(cfg, x, inv, q, s)
+    some = torch.cat([torch.arange(40), torch.arange(T - 40, T)]).cuda()
+    token = torch.empty_like(inv)
+    token[inv.long()] = torch.arange(T, dtype=torch.int32, device="cuda")
+    rq, rs = R.quantize(x[token[some].long()].cpu())
+    assert torch.equal(q[some].cpu().double(), rq) and torch.equal(s[some].cpu(), rs)
+    w = (torch.randn(E, H, 2 * D, generator=g, device="cuda", dtype=BF16) * 0.02)
+    w_q, w_s = torch.empty(E, 2 * D, H, dtype=torch.int8, device="cuda"), torch.empty(E, 2 * D, device="cuda")
+    abi.moe_quantize_weights(cfg, "gate_up", w, w_q, w_s)
+    assert E * 2 * D * H > 2 ** 31
+    rq, rs = R.quantize(w[-1, :, -30:].T.contiguous().cpu())
+    assert torch.equal(w_q[-1, -30:].cpu().double(), rq) and torch.equal(w_s[-1, -30:].cpu(), rs)
+    del w
+    bounds = torch.linspace(0, T, E + 1).to(torch.int32)
+    out = torch.zeros(T, D, dtype=BF16, device="cuda")
+    ws = torch.empty(abi.moe_operator_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    abi.moe_grouped_linear_int8(cfg, "gate_up", q, s, w_q, w_s, bounds.cuda(), out, ws)
+    assert abi.moe_device_status(ws) == 0
+    for rows, e in ((some[:40], 0), (some[40:], E - 1)):
+        ref, tol = R.linear_int8(q[rows].cpu(), s[rows].cpu(), w_q[e][None].cpu(), w_s[e][None].cpu(), None,
+                                 torch.tensor([0, 40]), "gate_up", "concatenated", "silu", 0.0, 0.0,
+                                 torch.zeros(40, D, dtype=BF16))
+        R.assert_within(out[rows], ref, tol, f"expert {e}")
+
+
 # ------------------------------------------------------------------ 8-bit
 QUANT = [(1, 8, 1), (3, 24, 2), (5, 520, 3), (2, 4096, 8), (7, 16400, 2), (4, 2880, 1), (600, 1000, 2), (450, 2888, 4),
          (333, 33000, 1)]
@@ -422,6 +506,28 @@ def test_grouped_linear_int8_non_finite_scales():
     assert torch.isnan(out[2]).all() and torch.isfinite(out[[0, 1, 3, 4]]).all() and (out[[0, 1, 3, 4], 7] == 0).all()
 
 
+@pytest.mark.parametrize("act,limit", [("silu", 0.0), ("silu", 2.0), ("swigluoai", 7.0), ("gelu_tanh", 0.0)])
+def test_grouped_linear_int8_nan_rows_stay_nan(act, limit):
+    """A row with a NaN scale gives a row of NaN through every activation and clamp."""
+    T, H, D, E = 70, 64, 40, 1
+    cfg = abi.config(T, H, E, 1, D, activation=act, alpha=R.ALPHA if act == "swigluoai" else 0.0, limit=limit)
+    q, w = torch.ones(T, H, dtype=torch.int8, device="cuda"), torch.ones(E, 2 * D, H, dtype=torch.int8, device="cuda")
+    s, w_s = torch.full((T,), 0.1, device="cuda"), torch.full((E, 2 * D), 0.1, device="cuda")
+    s[3] = s[69] = float("nan")
+    out = torch.zeros(T, D, dtype=BF16, device="cuda")
+    ws = torch.empty(abi.moe_operator_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    abi.moe_grouped_linear_int8(cfg, "gate_up", q, s, w, w_s, torch.tensor([0, T], dtype=torch.int32).cuda(), out, ws)
+    nan = torch.isnan(out).cpu()
+    want = torch.zeros(T, D, dtype=torch.bool)
+    want[[3, 69]] = True
+    assert torch.equal(nan, want)
+
+
+def test_grouped_linear_int8_largest_expert_count():
+    int8_case(700, 64, 72, 1024, 2, "gate_up", seed=3)
+    int8_case(700, 64, 72, 1024, 2, "down", drop=0.3, seed=4)
+
+
 @pytest.mark.parametrize("offsets", [[0, 9, 8, 10], [0, 4, 8, 11], [1, 4, 8, 10], [0, -3, 8, 10], [0, 2 ** 30, 5, 10]])
 def test_grouped_linear_int8_bad_offsets(offsets):
     """Offsets that are no CSR of at most R rows are recorded and nothing is written."""
@@ -565,6 +671,79 @@ def test_int8_layer(fmt, act, bias):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first)
+
+
+def test_row_gradients_against_differences():
+    """Dispatch and combine are linear in rows and weights, so a difference of the
+    forward pass is the gradient up to rounding: along random directions, fp32
+    outputs summed in 64 bits."""
+    T, H, E, k = 37, 136, 6, 3
+    cfg = abi.config(T, H, E, k, 8)
+    _, _, inv = R.routing(T, E, k, seed=4, drop=0.2)
+    inv = inv.cuda()
+    x, rows, w = randn(1, T, H).cuda(), randn(2, T * k, H).cuda(), randn(3, T, k).cuda()
+    dx, drows, dw = randn(4, T, H).cuda(), randn(5, T * k, H).cuda(), randn(6, T, k).cuda()
+    g_rows, g_out = randn(7, T * k, H).cuda(), randn(8, T, H).cuda()
+
+    def dispatch(x, w):
+        out = torch.zeros(T * k, H, device="cuda")
+        abi.moe_dispatch(cfg, x, inv, out, expert_weights=w)
+        return out.double()
+
+    def combine(rows, w):
+        out = torch.zeros(T, H, device="cuda")
+        abi.moe_combine(cfg, rows, inv, out, expert_weights=w)
+        return out.double()
+
+    b_x, b_w = torch.empty_like(x), torch.empty_like(w)
+    abi.moe_dispatch_backward(cfg, g_rows, inv, b_x, x=x, expert_weights=w, d_expert_weights=b_w)
+    c_rows, c_w = torch.zeros_like(rows), torch.empty_like(w)
+    abi.moe_combine_backward(cfg, g_out, inv, c_rows, rows=rows, expert_weights=w, d_expert_weights=c_w)
+    for f, a, da, grad, g in ((lambda v: dispatch(v, w), x, dx, b_x, g_rows), (lambda v: dispatch(x, v), w, dw, b_w, g_rows),
+                              (lambda v: combine(v, w), rows, drows, c_rows, g_out), (lambda v: combine(rows, v), w, dw, c_w, g_out)):
+        up, down = f(a + da), f(a - da)
+        diff = float(((up - down) / 2 * g.double()).sum())
+        along = float((grad.double() * da.double()).sum())
+        # each of the T*k*H terms of up and down rounds k + 3 times; the gradient sums H / 32 + 24 deep
+        size = float(((up.abs() + down.abs()) * g.double().abs()).sum()) + float((grad.double() * da.double()).abs().sum())
+        assert abs(diff - along) <= size * (k + 3 + H / 32 + 24) * R.F32
+
+
+def test_two_calls_at_once():
+    """The same operators on two streams at the same time, a workspace each."""
+    T, H, D, E, k = 500, 520, 264, 12, 2
+    cfg = abi.config(T, H, E, k, D)
+    jobs = []
+    for i in range(2):
+        _, off, inv = R.routing(T, E, k, seed=30 + i)
+        g = torch.Generator().manual_seed(i)
+        jobs.append(dict(
+            off=off.cuda(), inv=inv.cuda(), x=randn(i, T, H, dtype=BF16).cuda(),
+            w_q=torch.randint(-127, 128, (E, 2 * D, abi.int8_pitch(H)), generator=g, dtype=torch.int8).cuda(),
+            w_s=(torch.rand(E, 2 * D, generator=g) * 0.01).cuda(), stream=torch.cuda.Stream(),
+            q=torch.zeros(T * k, abi.int8_pitch(H), dtype=torch.int8, device="cuda"), s=torch.zeros(T * k, device="cuda"),
+            h=torch.zeros(T * k, D, dtype=BF16, device="cuda"),
+            ws=torch.empty(abi.moe_operator_workspace_size(cfg), dtype=torch.uint8, device="cuda")))
+
+    def run(j, stream=None):
+        abi.moe_dispatch_int8(cfg, j["x"], j["inv"], j["q"], j["s"], stream=stream)
+        abi.moe_grouped_linear_int8(cfg, "gate_up", j["q"], j["s"], j["w_q"], j["w_s"], j["off"], j["h"], j["ws"],
+                                    stream=stream)
+
+    want = []
+    for j in jobs:
+        run(j)
+        torch.cuda.synchronize()
+        want.append(j["h"].clone())
+    for j in jobs:
+        j["h"].zero_(), j["q"].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for j in jobs:
+            run(j, j["stream"])
+    torch.cuda.synchronize()
+    for j, w in zip(jobs, want):
+        assert torch.equal(j["h"], w) and abi.moe_device_status(j["ws"]) == 0
 
 
 def test_backward_captured_and_on_a_given_stream():

@@ -41,7 +41,7 @@ ROWS = {  # entry point -> its pointers in order: (name, required)
 def test_row_operators_refuse(lib, name):
     fn, args = getattr(lib, name), ROWS[name]
     c = cfg()
-    full = [FAKE] * len(args)
+    full = [FAKE + 0x1000 * i for i in range(len(args))]
     assert fn(ctypes.byref(c), 2, *full, None) == INVALID                     # no such row type
     for i, (arg, required) in enumerate(args):
         call = list(full)
@@ -52,6 +52,12 @@ def test_row_operators_refuse(lib, name):
         if arg not in ("inverse", "w", "d_w"):
             assert fn(ctypes.byref(c), F32, *call, None) == INVALID, arg
     assert fn(None, BF16, *full, None) == INVALID
+    names = [a for a, _ in args]
+    out = full[names.index({"moe_dispatch": "rows", "moe_combine": "out", "moe_dispatch_backward": "d_x",
+                            "moe_combine_backward": "d_rows"}[name])]
+    for i, arg in enumerate(names):                                           # no output in place of an input
+        if full[i] != out and arg not in ("inverse", "w", "d_w"):
+            assert fn(ctypes.byref(c), BF16, *[out if j == i else p for j, p in enumerate(full)], None) == INVALID
     assert fn(ctypes.byref(cfg(H=60)), BF16, *full, None) == UNSUPPORTED
     assert fn(ctypes.byref(cfg(T=0)), BF16, *([None] * len(args)), None) == 0  # no tokens: nothing to do
 
@@ -60,10 +66,10 @@ def test_route_backward_refuses(lib):
     by, need = ctypes.byref, abi.moe_operator_workspace_size(cfg())
     f = lib.moe_route_backward
 
-    def call(c, logits=FAKE, gs=None, idx=FAKE, dw=FAKE, ds=None, out=FAKE, dgs=None, ws=None, n=0):
+    def call(c, logits=FAKE, gs=None, idx=FAKE, dw=FAKE, ds=None, out=FAKE + 0x1000, dgs=None, ws=None, n=0):
         return f(by(c), logits, gs, idx, dw, ds, out, dgs, ws, n, None)
 
-    for kw in ({"logits": None}, {"idx": None}, {"dw": None}, {"out": None}):
+    for kw in ({"logits": None}, {"idx": None}, {"dw": None}, {"out": None}, {"out": FAKE}):
         assert call(cfg(), **kw) == INVALID
         assert call(sink(), **kw) == INVALID
     assert call(cfg(), gs=FAKE) == INVALID                 # the softmax router has no global scale
