@@ -251,6 +251,86 @@ __global__ void __launch_bounds__(kRowThreads) rows_dot_kernel(const RowsArgs a)
   }
 }
 
+// The same for short rows (at most G U vectors): G lanes per token, 32 / G
+// tokens a warp, the slots in batches of 8 that are loaded together; a batch's
+// inner products are summed over the G lanes, and lane q stores slot q's.
+// (16384 tokens of 64 bf16, k 16: 12.6 and 16.9 us where a warp or block per token
+// takes 42.3 (gather) and 102 us (spread).)
+template <bool F32, bool SPREAD, int G, int U>
+__global__ void __launch_bounds__(kRowThreads) rows_dot_short_kernel(const RowsArgs a) {
+  griddep_wait();  // the previous kernel's results are complete and visible
+  griddep_launch_dependents();
+  static_assert(G >= 8, "lane q of a group stores slot q of a batch");
+  constexpr int N = Vec<F32>::N;
+  constexpr int KB = 8;
+  const int64_t t = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) / G;
+  const int i = threadIdx.x & (G - 1);
+  const bool live = t < a.T;  // (every lane takes part in the sums)
+  const uint4* rows = static_cast<const uint4*>(a.rows_in);
+  Vec<F32> x[U], acc[U];
+#pragma unroll
+  for (int v = 0; v < U; ++v) {
+    const int c = i + v * G;
+    x[v].unpack(live && c < a.vec ? __ldg(static_cast<const uint4*>(a.tok_in) + t * a.vec + c) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[v].v[e] = 0.f;
+  }
+  for (int j0 = 0; j0 < a.k; j0 += KB) {
+    int p[KB];
+    float w[KB], dot[KB];
+    if (live) {
+      load_slots<KB>(a, t, j0, p, w);
+    } else {
+#pragma unroll
+      for (int q = 0; q < KB; ++q) p[q] = -1;
+    }
+    uint4 u[U][KB];
+#pragma unroll
+    for (int v = 0; v < U; ++v)
+#pragma unroll
+      for (int q = 0; q < KB; ++q)
+        u[v][q] = p[q] >= 0 && i + v * G < a.vec ? __ldg(rows + static_cast<int64_t>(p[q]) * a.vec + i + v * G)
+                                                 : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < KB; ++q) {
+      dot[q] = 0.f;
+      if (p[q] < 0) continue;
+#pragma unroll
+      for (int v = 0; v < U; ++v) {
+        const int c = i + v * G;
+        Vec<F32> y, o;
+        y.unpack(u[v][q]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          dot[q] += x[v].v[e] * y.v[e];
+          if constexpr (SPREAD) o.v[e] = w[q] * x[v].v[e];
+          else acc[v].v[e] += w[q] * y.v[e];
+        }
+        if constexpr (SPREAD) {
+          if (c < a.vec) static_cast<uint4*>(a.rows_out)[static_cast<int64_t>(p[q]) * a.vec + c] = o.pack();
+        }
+      }
+    }
+    float mine = 0.f;
+#pragma unroll
+    for (int q = 0; q < KB; ++q) {
+      if (j0 + q < a.k) {  // (the same for the whole grid)
+#pragma unroll
+        for (int off = G / 2; off > 0; off >>= 1) dot[q] += __shfl_xor_sync(0xffffffffu, dot[q], off);
+        if (i == q) mine = dot[q];
+      }
+    }
+    if (live && i < KB && j0 + i < a.k) a.d_weights[t * a.k + j0 + i] = mine;
+  }
+  if constexpr (!SPREAD) {
+#pragma unroll
+    for (int v = 0; v < U; ++v) {
+      const int c = i + v * G;
+      if (live && c < a.vec) static_cast<uint4*>(a.tok_out)[t * a.vec + c] = acc[v].pack();
+    }
+  }
+}
+
 // out[t] = sum_j w * rows[p] (and the weights' gradient, DOT) for many tokens,
 // through a ring in shared memory.  A warp walks whole tokens (or, without
 // DOT, segments of them), 32 columns a step; each thread copies the k (+ 1)
@@ -261,16 +341,23 @@ __global__ void __launch_bounds__(kRowThreads) rows_dot_kernel(const RowsArgs a)
 // loads wait for their positions and drain at each token, reached 4.7 TB/s
 // on them.
 constexpr int kRingThreads = 256;
-constexpr int kRingBytes = 104 * 1024;  // two blocks a SM
+constexpr int kRingBytes = 104 * 1024;  // of a block of 256 threads, two a SM
 
+// Where three steps of 256 threads do not fit, half the threads and as many
+// blocks as fit: a step of nine rows and more is long, and it is warps that
+// hide it (16384 x 1024, k 8: 71.4 us with 2 blocks of 5 steps, 53.8 with 4 of
+// 3; with fewer rows the deeper ring of two blocks is the better, 8192 x 2880,
+// k 4: 38.7 and 40.9 us).
 template <int KB, bool DOT>
 struct Ring {
   static constexpr int ROWS = KB + (DOT ? 1 : 0);
-  static constexpr int THREADS = ROWS * kRingThreads * 16 * 3 <= kRingBytes ? kRingThreads : kRingThreads / 2;
+  static constexpr bool WIDE = ROWS * kRingThreads * 16 * 3 <= kRingBytes;
+  static constexpr int THREADS = WIDE ? kRingThreads : kRingThreads / 2;
   static constexpr int FIT = kRingBytes / (ROWS * THREADS * 16);
-  static constexpr int S = FIT < 8 ? FIT : 8;
+  static constexpr int S = !WIDE ? 3 : FIT < 8 ? FIT : 8;
   static constexpr int BYTES = S * ROWS * THREADS * 16;
-  static_assert(S >= 2, "a ring of two steps at least");
+  static constexpr int BLOCKS = WIDE ? 2 : 222 * 1024 / (BYTES + 1024);  // of a SM
+  static_assert(S >= 3 && BLOCKS >= 2, "the ring fits a SM");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -408,7 +495,7 @@ cudaError_t launch_ring(const RowsArgs& a, cudaStream_t stream) {
   const cudaError_t err =
       opt_in_dynamic_smem(reinterpret_cast<const void*>(gather_ring_kernel<F32, DOT, KB>), G::BYTES);
   if (err != cudaSuccess) return err;
-  const int64_t most = static_cast<int64_t>(a.num_sms) * 2 * kWarps;  // warps resident at once
+  const int64_t most = static_cast<int64_t>(a.num_sms) * G::BLOCKS * kWarps;  // warps resident at once
   // without the weights' gradient a token may be cut into segments of whole
   // 32-column steps, so that every warp has several jobs
   int segs = 1;
@@ -459,6 +546,25 @@ cudaError_t launch_dot(const RowsArgs& a, cudaStream_t stream) {
   return launch_dot_k<F32, SPREAD, 32, 1>(a, stream);
 }
 
+template <bool F32, bool SPREAD, int G, int U>
+cudaError_t launch_short(const RowsArgs& a, cudaStream_t stream) {
+  const int64_t blocks = (static_cast<int64_t>(a.T) * G + kRowThreads - 1) / kRowThreads;
+  return launch_pdl(rows_dot_short_kernel<F32, SPREAD, G, U>, dim3(static_cast<unsigned>(blocks)), dim3(kRowThreads), 0,
+                    stream, a);
+}
+
+template <bool F32, bool SPREAD>
+cudaError_t launch_grad(const RowsArgs& a, cudaStream_t stream) {
+  if (a.vec <= 8) return launch_short<F32, SPREAD, 8, 1>(a, stream);
+  if (a.vec <= 16) return launch_short<F32, SPREAD, 16, 1>(a, stream);
+  if (a.vec <= 32) return launch_short<F32, SPREAD, 32, 1>(a, stream);
+  if constexpr (!SPREAD) {
+    if (a.vec <= 64) return launch_short<F32, SPREAD, 32, 2>(a, stream);
+    if (use_ring(a)) return launch_ring_k<F32, true>(a, stream);
+  }
+  return launch_dot<F32, SPREAD>(a, stream);
+}
+
 template <bool F32, int KB, int U>
 cudaError_t launch_copy(const RowsArgs& a, bool spread, cudaStream_t stream) {
   const Tiling tl = tiling(a.vec, spread ? 1 : U);
@@ -473,10 +579,9 @@ cudaError_t launch_copy(const RowsArgs& a, bool spread, cudaStream_t stream) {
 
 template <bool F32>
 cudaError_t launch_rows(const RowsArgs& a, bool spread, cudaStream_t stream) {
-  if (!spread && use_ring(a))
-    return a.d_weights != nullptr ? launch_ring_k<F32, true>(a, stream) : launch_ring_k<F32, false>(a, stream);
   if (a.d_weights != nullptr)
-    return spread ? launch_dot<F32, true>(a, stream) : launch_dot<F32, false>(a, stream);
+    return spread ? launch_grad<F32, true>(a, stream) : launch_grad<F32, false>(a, stream);
+  if (!spread && use_ring(a)) return launch_ring_k<F32, false>(a, stream);
   // two columns a thread pay for one or two rows (4096 x 4096, k 2: 21.4 -> 19.9 us), more do not, and for more
   // rows a column is enough (2048 x 2880, k 4: 12.6 us with one, 17.7 with two); loads that k does not fill cost too
   // (8192 x 2048, k 6: 47.4 us with eight, 39.9 with six)

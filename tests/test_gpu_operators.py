@@ -130,7 +130,8 @@ def _all_rows(cfg, x, rows, w, inv, T, H, k):
 @pytest.mark.parametrize("T,H,E,k,drop,dtype", [
     (5003, 1544, 128, 6, 0.0, BF16), (5003, 1544, 128, 6, 0.0, F32), (8209, 4104, 8, 2, 0.0, BF16),
     (1100, 2056, 40, 3, 0.3, F32), (1025, 1000, 30, 16, 0.1, BF16), (4097, 2184, 16, 8, 0.2, BF16),
-    (12007, 264, 9, 4, 0.1, BF16), (16500, 24, 3, 1, 0.0, F32)])
+    (12007, 264, 9, 4, 0.1, BF16), (16500, 24, 3, 1, 0.0, F32),
+    (3001, 2056, 12, 7, 0.1, BF16), (5000, 128, 20, 19, 0.1, BF16), (2500, 256, 40, 32, 0.1, F32), (3000, 480, 9, 5, 0.2, BF16)])
 def test_rows_large(T, H, E, k, drop, dtype):
     """Tokens by the thousand, ragged, the same bits on every run."""
     cfg = abi.config(T, H, E, k, 8)
