@@ -8,6 +8,7 @@
 // 2^-9 away from one, far beyond the reciprocal's error; the ties are a = m/2
 // (63.5, to 64) and those of an m whose reciprocal times 127 is a power of two
 // (exact).  The reciprocal is rounded up, so 63.5 never falls below its tie.
+// Bound by HBM: each value read once and each place written once.
 // Rows of denormal size are scaled by 2^64 first.  A row that holds an
 // infinity or a NaN gets a NaN scale, so that its products are NaN.
 #include <algorithm>
@@ -125,7 +126,11 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv
 // Weights [E, K, N] bf16 to [E, N, pitch] 8-bit, one scale per column.  A
 // block owns 64 columns of one expert: it reads its K x 64 strip for the
 // maxima, and again (from L2, mostly) to round it, turning 128 x 64 blocks
-// through shared memory so that both sides move whole sectors.
+// through shared memory so that both sides move whole sectors.  E 8, 4096 x
+// 28672 in 737 us, 0.58 of the copy rate: the strips of all blocks together do
+// not stay in L2 between the two readings.  One block of 1024 threads a SM,
+// whose strips would (936 us), and a cluster that holds its strip in shared
+// memory (1176 us) were slower, and this runs once per model.
 constexpr int kWCols = 64, kWRows = 128, kWThreads = 256;
 constexpr int kWPitch = kWRows + 4;  // bytes; a word stride of 33
 

@@ -13,7 +13,10 @@
 // Bound by the store of the dense [T, E + S] gradient and by instruction
 // issue: W lanes (the smallest power of two that holds the n entries) work on
 // a token, so a warp works on 32 / W, and its rows are zeroed in 16-byte
-// stores while the entries' loads are in flight; the entries follow.
+// stores while the entries' loads are in flight; the entries follow.  8192
+// tokens of 128 + 2 lanes take 3.6 us, 4.8 with the global scale's gradient (a
+// second launch that sums the blocks' parts in order); a warp per token that
+// built its row in shared memory took 8.0 and 9.4.
 #include <algorithm>
 
 #include "kernels.cuh"

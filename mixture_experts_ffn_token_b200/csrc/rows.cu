@@ -11,7 +11,11 @@
 // in a fixed order: results are the same bits on every run.
 //
 // All of them are bound by HBM: per token one row on the token side and k
-// rows on the sorted side, each moved once.
+// rows on the sorted side, each moved once.  On one B200 (6.56 TB/s copy rate),
+// bf16: dispatch 8192 x 2048, k 6 in 38.1 us (0.94 of that rate), its gradient
+// with the weights' 45.5 us (0.90), combine 38.8 us (0.92), its gradient with
+// the weights' 74.2 us (0.90).  A few megabytes take launch, first loads and last
+// wave, 2 to 4 us (combine 2048 x 2880, k 4: 12.3 us, 9.0 at the copy rate).
 #include <algorithm>
 
 #include "kernels.cuh"
