@@ -163,95 +163,109 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const RowsArgs a
 
 // The same with the weights' gradient: one block per token, its k inner
 // products reduced over the block in a fixed order.  SPREAD: rows[p] =
-// w * tok[t] is written; else out[t] = sum_j w * rows[p] (KB >= k terms, kept
-// in registers so that every row is read once).  A thread loads U columns of
-// up to 8 / U rows before it uses the first.  A row of at most 32 U vectors is
+// w * tok[t] is written, with BATCHES `step` <= KB slots at a time, each time
+// reading the token's row again (from L1); else out[t] = sum_j w * rows[p] (KB >= k terms, kept in
+// registers so that every row is read once).  A thread loads U columns of up
+// to 8 / U rows before it uses the first.  A row of at most 32 U vectors is
 // a warp's (blockDim.y tokens a block, no sum across warps).
-template <bool F32, bool SPREAD, int KB, int U>
-__global__ void __launch_bounds__(kRowThreads) rows_dot_kernel(const RowsArgs a) {
+template <bool F32, bool SPREAD, int KB, int U, bool BATCHES>
+__global__ void __launch_bounds__(kRowThreads) rows_dot_kernel(const RowsArgs a, int step) {
+  static_assert(!BATCHES || SPREAD, "only spreading may take the slots in batches");
   griddep_wait();  // the previous kernel's results are complete and visible
   griddep_launch_dependents();
   __shared__ float s_part[kRowThreads / 32][KB];
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (t >= a.T) return;  // (whole warps, and then nothing is synchronised)
-  int p[KB];
-  float w[KB];
-  load_slots<KB>(a, t, 0, p, w);
   const uint4* tok = static_cast<const uint4*>(a.tok_in) + t * a.vec;
   const uint4* rows = static_cast<const uint4*>(a.rows_in);
   constexpr int N = Vec<F32>::N;
   constexpr int kBatch = KB < 8 ? KB : 8;
-  float dot[KB];
+  for (int b0 = 0; b0 < (BATCHES ? a.k : 1); b0 += BATCHES ? step : 1) {
+    int p[KB];
+    float w[KB];
+    load_slots<KB>(a, t, b0, p, w);
+    const int count = BATCHES ? min(step, a.k - b0) : a.k;
+    if constexpr (BATCHES) {
 #pragma unroll
-  for (int j = 0; j < KB; ++j) dot[j] = 0.f;
-  for (int c0 = tid; c0 < a.vec; c0 += U * blockDim.x) {
-    uint4 ux[U];
-    Vec<F32> x[U], acc[U];
-#pragma unroll
-    for (int v = 0; v < U; ++v) {
-      const int c = c0 + v * blockDim.x;
-      ux[v] = c < a.vec ? __ldg(tok + c) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < KB; ++j)
+        if (j >= count) p[j] = -1;  // the next batch's
     }
+    float dot[KB];
 #pragma unroll
-    for (int j0 = 0; j0 < KB; j0 += kBatch) {
-      uint4 u[U][kBatch];
+    for (int j = 0; j < KB; ++j) dot[j] = 0.f;
+    for (int c0 = tid; c0 < a.vec; c0 += U * blockDim.x) {
+      uint4 ux[U];
+      Vec<F32> x[U], acc[U];
 #pragma unroll
       for (int v = 0; v < U; ++v) {
         const int c = c0 + v * blockDim.x;
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q)
-          u[v][q] = p[j0 + q] >= 0 && c < a.vec ? __ldg(rows + static_cast<int64_t>(p[j0 + q]) * a.vec + c)
-                                                : make_uint4(0, 0, 0, 0);
+        ux[v] = c < a.vec ? __ldg(tok + c) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int v = 0; v < U; ++v) {
-        const int c = c0 + v * blockDim.x;
-        if (j0 == 0) {
-          x[v].unpack(ux[v]);
+      for (int j0 = 0; j0 < KB; j0 += kBatch) {
+        uint4 u[U][kBatch];
 #pragma unroll
-          for (int i = 0; i < N; ++i) acc[v].v[i] = 0.f;
+        for (int v = 0; v < U; ++v) {
+          const int c = c0 + v * blockDim.x;
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q)
+            u[v][q] = p[j0 + q] >= 0 && c < a.vec ? __ldg(rows + static_cast<int64_t>(p[j0 + q]) * a.vec + c)
+                                                  : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          if (p[j0 + q] < 0) continue;
-          Vec<F32> y, o;
-          y.unpack(u[v][q]);
+        for (int v = 0; v < U; ++v) {
+          const int c = c0 + v * blockDim.x;
+          if (j0 == 0) {
+            x[v].unpack(ux[v]);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            dot[j0 + q] += x[v].v[i] * y.v[i];
-            if constexpr (SPREAD) o.v[i] = w[j0 + q] * x[v].v[i];
-            else acc[v].v[i] += w[j0 + q] * y.v[i];
+            for (int i = 0; i < N; ++i) acc[v].v[i] = 0.f;
           }
-          if constexpr (SPREAD) {
-            if (c < a.vec) static_cast<uint4*>(a.rows_out)[static_cast<int64_t>(p[j0 + q]) * a.vec + c] = o.pack();
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            if (p[j0 + q] < 0) continue;
+            Vec<F32> y, o;
+            y.unpack(u[v][q]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              dot[j0 + q] += x[v].v[i] * y.v[i];
+              if constexpr (SPREAD) o.v[i] = w[j0 + q] * x[v].v[i];
+              else acc[v].v[i] += w[j0 + q] * y.v[i];
+            }
+            if constexpr (SPREAD) {
+              if (c < a.vec) static_cast<uint4*>(a.rows_out)[static_cast<int64_t>(p[j0 + q]) * a.vec + c] = o.pack();
+            }
           }
         }
       }
-    }
-    if constexpr (!SPREAD) {
+      if constexpr (!SPREAD) {
 #pragma unroll
-      for (int v = 0; v < U; ++v) {
-        const int c = c0 + v * blockDim.x;
-        if (c < a.vec) static_cast<uint4*>(a.tok_out)[t * a.vec + c] = acc[v].pack();
+        for (int v = 0; v < U; ++v) {
+          const int c = c0 + v * blockDim.x;
+          if (c < a.vec) static_cast<uint4*>(a.tok_out)[t * a.vec + c] = acc[v].pack();
+        }
       }
     }
-  }
 #pragma unroll
-  for (int j = 0; j < KB; ++j) {
-    float v = dot[j];
+    for (int j = 0; j < KB; ++j) {
+      float v = dot[j];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (lane == 0) s_part[threadIdx.y + warp][j] = v;
-  }
-  if (blockDim.y > 1) __syncwarp();
-  else __syncthreads();
-  const int warps = blockDim.x >> 5;
-  for (int j = tid; j < a.k; j += blockDim.x) {
-    const int pj = a.inverse[t * a.k + j];
-    float v = 0.f;
-    for (int i = 0; i < warps; ++i) v += s_part[threadIdx.y + i][j];
-    a.d_weights[t * a.k + j] = pj >= 0 && pj < a.R ? v : 0.f;
+      for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+      if (lane == 0) s_part[threadIdx.y + warp][j] = v;
+    }
+    if (blockDim.y > 1) __syncwarp();
+    else __syncthreads();
+    const int warps = blockDim.x >> 5;
+    for (int j = tid; j < count; j += blockDim.x) {
+      const int pj = a.inverse[t * a.k + b0 + j];
+      float v = 0.f;
+      for (int i = 0; i < warps; ++i) v += s_part[threadIdx.y + i][j];
+      a.d_weights[t * a.k + b0 + j] = pj >= 0 && pj < a.R ? v : 0.f;
+    }
+    if constexpr (BATCHES) {  // the parts are read before the next batch's
+      if (blockDim.y > 1) __syncwarp();
+      else __syncthreads();
+    }
   }
 }
 
@@ -482,14 +496,14 @@ __global__ void __launch_bounds__(kRingThreads) gather_ring_kernel(const RowsArg
   }
 }
 
-template <bool F32, bool SPREAD, int KB, int U>
-cudaError_t launch_dot_k(const RowsArgs& a, cudaStream_t stream) {
+template <bool F32, bool SPREAD, int KB, int U, bool BATCHES = false>
+cudaError_t launch_dot_k(const RowsArgs& a, int step, cudaStream_t stream) {
   // whole warps that cover the row in the fewest equal steps
-  const int steps = (a.vec + kRowThreads * U - 1) / (kRowThreads * U);
-  const int threads = ((a.vec + steps * U - 1) / (steps * U) + 31) / 32 * 32;
+  const int rounds = (a.vec + kRowThreads * U - 1) / (kRowThreads * U);
+  const int threads = ((a.vec + rounds * U - 1) / (rounds * U) + 31) / 32 * 32;
   const int tokens = threads == 32 ? kRowThreads / 32 : 1;
-  return launch_pdl(rows_dot_kernel<F32, SPREAD, KB, U>, dim3(static_cast<unsigned>((a.T + tokens - 1) / tokens)),
-                    dim3(static_cast<unsigned>(threads), static_cast<unsigned>(tokens)), 0, stream, a);
+  return launch_pdl(rows_dot_kernel<F32, SPREAD, KB, U, BATCHES>, dim3(static_cast<unsigned>((a.T + tokens - 1) / tokens)),
+                    dim3(static_cast<unsigned>(threads), static_cast<unsigned>(tokens)), 0, stream, a, step);
 }
 
 template <bool F32, bool DOT, int KB>
@@ -541,13 +555,20 @@ bool use_ring(const RowsArgs& a) {
 
 template <bool F32, bool SPREAD>
 cudaError_t launch_dot(const RowsArgs& a, cudaStream_t stream) {
-  if (a.k <= 1) return launch_dot_k<F32, SPREAD, 1, 4>(a, stream);
-  if (a.k <= 2) return launch_dot_k<F32, SPREAD, 2, 4>(a, stream);
-  if (a.k <= 4) return launch_dot_k<F32, SPREAD, 4, 2>(a, stream);
-  if (a.k <= 6) return launch_dot_k<F32, SPREAD, 6, 1>(a, stream);
-  if (a.k <= 8) return launch_dot_k<F32, SPREAD, 8, 1>(a, stream);
-  if (a.k <= 16) return launch_dot_k<F32, SPREAD, 16, 1>(a, stream);
-  return launch_dot_k<F32, SPREAD, 32, 1>(a, stream);
+  if (a.k <= 1) return launch_dot_k<F32, SPREAD, 1, 4>(a, a.k, stream);
+  if (a.k <= 2) return launch_dot_k<F32, SPREAD, 2, 4>(a, a.k, stream);
+  if (a.k <= 4) return launch_dot_k<F32, SPREAD, 4, 2>(a, a.k, stream);
+  if (a.k <= 6) return launch_dot_k<F32, SPREAD, 6, 1>(a, a.k, stream);
+  if (a.k <= 8) return launch_dot_k<F32, SPREAD, 8, 1>(a, a.k, stream);
+  if constexpr (SPREAD) {
+    // equal batches of at most 8
+    const int batches = (a.k + 7) / 8, step = (a.k + batches - 1) / batches;
+    if (step <= 6) return launch_dot_k<F32, true, 6, 1, true>(a, step, stream);
+    return launch_dot_k<F32, true, 8, 1, true>(a, step, stream);
+  } else {
+    if (a.k <= 16) return launch_dot_k<F32, false, 16, 1>(a, a.k, stream);
+    return launch_dot_k<F32, false, 32, 1>(a, a.k, stream);
+  }
 }
 
 template <bool F32, bool SPREAD, int G, int U>
