@@ -12,8 +12,8 @@
 //
 // One persistent CTA per SM, as in the bf16 kernel:
 //   warp 0      TMA producer: per 128-wide K block one 128 x 128 B box of A
-//               (64 or 16 rows for a tile of at most so many) and one 256 x
-//               128 B tile of W into a 4-stage ring;
+//               (64 rows for a tile of at most 64) and one 256 x 128 B tile of
+//               W into a 4-stage ring;
 //   warp 1      MMA issuer: four tcgen05.mma kind::i8 128x256x32 a stage
 //               (M = 64 for a tile of at most 64 rows), two 256-column
 //               accumulators alternate between tiles;
@@ -21,21 +21,17 @@
 // Tiles walk the column blocks of an expert, row pieces innermost, so that
 // CTAs running together share a weight block through L2.
 //
-// What bounds it, on one B200 (6.56 TB/s copy rate):
-//   few rows per expert   the weights' stream: E 128, 2880 x 5760, 8192 rows in
-//               341 us (6.4 TB/s); E 64, 1536 x 4096, 256 rows in 56 us, of
-//               which 5 us pass before the first copy has landed and 1.4 us are
-//               the seventh wave of 6.8; one token to 8 experts 13.8 us;
-//   many rows   the 1000 W power limit: E 8, 4096 x 28672, 8192 rows in 0.84 ms
-//               (2.3 POP/s) at 1.38 GHz in a loop, 0.71 ms (2.7) for a few
-//               passes; 0.65 ms with all-zero weights at 1.965 GHz.  Pairs of CTAs
-//               (256 x 256 tiles) drew the same power for the same time.
+// What bounds it, on one B200: with a long K the 1000 W power limit (E 8, 4096 x
+// 28672, 8192 rows in 0.84 ms, 2.3 POP/s, at 1.38 GHz in a loop, 0.71 ms for a few
+// passes, 0.65 ms with all-zero weights at 1.965 GHz; pairs of CTAs with 256 x
+// 256 tiles drew the same power for the same time), with a short one the
+// epilogue, whose shared-memory traffic fills 60% of its cycles (E 50, 240 x 2328,
+// 32200 rows in 66 us, 30 at the copy rate).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 
-#include "grouped_tiles.cuh"
-#include "kernels.cuh"
+#include "int8_common.cuh"
 
 namespace moe {
 namespace {
@@ -43,70 +39,16 @@ namespace {
 constexpr int BM = 128;                    // rows per tile (TMEM lanes)
 constexpr int BN = 256;                    // accumulator columns per tile
 constexpr int BK = 128;                    // K per stage: one 128-byte swizzle row
-constexpr int UMMA_K = 32;                 // K per tcgen05.mma (kind::i8)
 constexpr int A_BYTES = BM * BK;           // 16 KB
 constexpr int B_BYTES = BN * BK;           // 32 KB
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 4;
 constexpr int HALF_ROWS = 64;              // tiles of at most 64 rows: M = 64
-constexpr int FEW_ROWS = 16;               // tiles that copy only 16 rows of A
+constexpr int HALF_A_BYTES = HALF_ROWS * BK;
 constexpr int NUM_EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + 32 * NUM_EPI_WARPS;
 constexpr int CTRL_BYTES = 256;
 constexpr uint32_t TMEM_COLS = 2 * BN;     // two accumulators
-
-// Instruction descriptor for kind::i8, signed A and B, both K-major, 32-bit
-// integer D: D format bits 4..5 = 2 (s32), A format 7..9 = 1 (s8), B format
-// 10..12 = 1 (s8), N >> 3 at 17..22, M >> 4 at 24..28.
-__host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-constexpr int MODE_CONCAT = 0;       // gate_up, [gate | up] columns
-constexpr int MODE_INTERLEAVED = 1;  // gate_up, gate on even columns
-constexpr int MODE_DOWN = 2;
-
-struct Int8Params {
-  const int32_t* offsets;
-  const float* a_scales;
-  const float* w_scales;
-  const __nv_bfloat16* bias;
-  __nv_bfloat16* out;
-  int* status;
-  int E, R;
-  int N;        // weight columns of an expert (2D or H)
-  int out_cols; // D or H
-  int n_tiles, num_kb;
-  int activation;
-  float alpha, limit;
-  int err_bit;
-};
-
-// The gated activation with sigmoids throughout (0.5 (1 + tanh a) is
-// sigmoid(2a)): exp2 and reciprocal approximations of about 2^-22, below the
-// bf16 rounding of h.  For large negative gates the exponential overflows and
-// the quotient is 0, as the limit is.
-__device__ __forceinline__ float gated(int act, float g, float u, float alpha, float limit) {
-  if (act != 2 && limit > 0.f) {
-    // (comparisons, so that a NaN stays one)
-    g = g > limit ? limit : g;
-    u = u > limit ? limit : u < -limit ? -limit : u;
-  }
-  if (act == 0) return __fdividef(g, 1.f + __expf(-g)) * u;
-  if (act == 1) return __fdividef(g, 1.f + __expf(-alpha * g)) * (u + 1.f);
-  return __fdividef(g, 1.f + __expf(-1.5957691216057308f * (g + 0.044715f * g * g * g))) * u;
-}
 
 // What one epilogue warp does of a tile: Cols::n output columns from column
 // `col` on, whose accumulators start at TMEM column `tcol` (concatenated: the up
@@ -130,12 +72,19 @@ __device__ __forceinline__ Part warp_part(int tile_n, int quad, int part, bool h
           half ? quad * 16 : quad * 32, half ? 16 : 32};
 }
 
-// A warp's weight columns, in groups of four: group i's scales lie in the 16
-// bytes that row i of its staging block leaves free, its biases behind the
-// block.  The loads are issued while the tile's product is still running,
-// since the scales come from HBM.  Concatenated: the gate columns' groups,
-// then the up columns'.
-constexpr int kWarpStage = kStageWarpBytes + 256;
+// An epilogue warp's shared memory: a block of 32 rows x 64 B that turns 32 x 32
+// outputs, its 128 weight columns' scales, and their biases.  16-byte piece c
+// of the block's row r lies at piece c ^ (r / 2 % 4), so that neither a piece of
+// eight rows nor four pieces of two rows meet in a bank.
+constexpr int kScalesAt = 32 * 64, kBiasAt = kScalesAt + 128 * 4;
+constexpr int kWarpStage = kBiasAt + 128 * 2;
+__device__ __forceinline__ uint8_t* turned(uint8_t* stage, int r, int c) {
+  return stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// The scales and biases are fetched in groups of four columns, one a lane, while
+// the tile's product is still running, since they come from HBM.
+// Concatenated: the gate columns' groups, then the up columns'.
 
 template <int MODE>
 __device__ __forceinline__ void stage_columns(const Int8Params& p, const Part& w, int e, int lane, uint8_t* stage) {
@@ -155,8 +104,8 @@ __device__ __forceinline__ void stage_columns(const Int8Params& p, const Part& w
     if (p.bias != nullptr) b = __ldg(reinterpret_cast<const uint2*>(p.bias + at));
   }
   __syncwarp();  // every lane is done with the tile before
-  *reinterpret_cast<float4*>(stage + lane * kStageRowBytes + 64) = s;
-  *reinterpret_cast<uint2*>(stage + kStageWarpBytes + 8 * lane) = b;
+  *reinterpret_cast<float4*>(stage + kScalesAt + 16 * lane) = s;
+  *reinterpret_cast<uint2*>(stage + kBiasAt + 8 * lane) = b;
   __syncwarp();
 }
 
@@ -164,100 +113,96 @@ struct Col4 {
   float s[4], b[4];
 };
 __device__ __forceinline__ Col4 columns(const uint8_t* stage, int i) {
-  const float4 s = *reinterpret_cast<const float4*>(stage + i * kStageRowBytes + 64);
-  const uint2 b = *reinterpret_cast<const uint2*>(stage + kStageWarpBytes + 8 * i);
+  const float4 s = *reinterpret_cast<const float4*>(stage + kScalesAt + 16 * i);
+  const uint2 b = *reinterpret_cast<const uint2*>(stage + kBiasAt + 8 * i);
   return {{s.x, s.y, s.z, s.w}, {bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y)}};
 }
 
 __device__ __forceinline__ float scaled(uint32_t acc, float row, const Col4& c, int i) {
-  return fmaf(static_cast<float>(static_cast<int>(acc)) * row, c.s[i], c.b[i]);
+  return int8_scaled(acc, row, c.s[i], c.b[i]);
 }
 
-// 32 output columns of this thread's row, from column `rel` of the warp's
-// columns, packed to bf16.
-template <int MODE>
-__device__ __forceinline__ void out_chunk(const Int8Params& p, const Part& w, uint32_t tacc, int rel, float row,
-                                          const uint8_t* stage, uint32_t (&packed)[16]) {
-  const int i0 = rel >> 2;
+// 16 outputs of this thread's row, from column `rel` of the warp's columns.
+template <int MODE, int ACT>
+__device__ __forceinline__ void outputs(const Int8Params& p, const Part& w, uint32_t tacc, int rel, float row,
+                                        const uint8_t* stage, float (&h)[16]) {
   if constexpr (MODE == MODE_DOWN) {
-    uint32_t a[32];
-    tmem_ld32(tacc + w.tcol + rel, a);
+    uint32_t a[16];
+    tmem_ld16(tacc + w.tcol + rel, a);
     tmem_ld_wait();
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const Col4 c = columns(stage, i0 + (j >> 2));
-      packed[j / 2] = pack_bf16x2(scaled(a[j], row, c, 0), scaled(a[j + 1], row, c, 1));
-      packed[j / 2 + 1] = pack_bf16x2(scaled(a[j + 2], row, c, 2), scaled(a[j + 3], row, c, 3));
+    for (int j = 0; j < 16; j += 4) {
+      const Col4 c = columns(stage, (rel + j) >> 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[j + i] = scaled(a[j + i], row, c, i);
     }
   } else if constexpr (MODE == MODE_CONCAT) {
-    uint32_t g[32], u[32];
-    tmem_ld32(tacc + w.tcol + rel, g);
-    tmem_ld32(tacc + w.tcol + BN / 2 + rel, u);
+    uint32_t g[16], u[16];
+    tmem_ld16(tacc + w.tcol + rel, g);
+    tmem_ld16(tacc + w.tcol + BN / 2 + rel, u);
     tmem_ld_wait();
-    const int i1 = i0 + 16;
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const Col4 cg = columns(stage, i0 + (j >> 2)), cu = columns(stage, i1 + (j >> 2));
-      float h[4];
+    for (int j = 0; j < 16; j += 4) {
+      const Col4 cg = columns(stage, (rel + j) >> 2), cu = columns(stage, 16 + ((rel + j) >> 2));
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        h[i] = gated(p.activation, scaled(g[j + i], row, cg, i), scaled(u[j + i], row, cu, i), p.alpha, p.limit);
-      packed[j / 2] = pack_bf16x2(h[0], h[1]);
-      packed[j / 2 + 1] = pack_bf16x2(h[2], h[3]);
+        h[j + i] = gated<ACT>(scaled(g[j + i], row, cg, i), scaled(u[j + i], row, cu, i), p.alpha, p.limit);
     }
   } else {
-    uint32_t a[64];
+    uint32_t a[32];
     tmem_ld32(tacc + w.tcol + 2 * rel, a);
-    tmem_ld32(tacc + w.tcol + 2 * rel + 32, a + 32);
     tmem_ld_wait();
 #pragma unroll
-    for (int j = 0; j < 64; j += 4) {
-      const Col4 c = columns(stage, 2 * i0 + (j >> 2));
-      const float h0 = gated(p.activation, scaled(a[j], row, c, 0), scaled(a[j + 1], row, c, 1), p.alpha, p.limit);
-      const float h1 = gated(p.activation, scaled(a[j + 2], row, c, 2), scaled(a[j + 3], row, c, 3), p.alpha, p.limit);
-      packed[j / 4] = pack_bf16x2(h0, h1);
+    for (int j = 0; j < 32; j += 4) {
+      const Col4 c = columns(stage, (2 * rel + j) >> 2);
+      h[j / 2] = gated<ACT>(scaled(a[j], row, c, 0), scaled(a[j + 1], row, c, 1), p.alpha, p.limit);
+      h[j / 2 + 1] = gated<ACT>(scaled(a[j + 2], row, c, 2), scaled(a[j + 3], row, c, 3), p.alpha, p.limit);
     }
   }
 }
 
 // One tile's epilogue for one warp, rs its thread's row scale; row0 the tile's
-// first row and rows how many there are.  Each 32 x 32 block is turned through the staging block so that a store instruction writes 8 rows
-// x 64 contiguous bytes.
-template <int MODE>
+// first row and rows how many there are.  Each 32 x 32 block is turned through
+// the staging block so that a store instruction writes 8 rows x 64 contiguous
+// bytes.  The loops stay rolled at 16 outputs: unrolled further the code
+// outgrows the instruction cache that ten warps share.
+template <int MODE, int ACT>
 __device__ __forceinline__ void epilogue(const Int8Params& p, const Part& w, uint32_t tacc, int row0, int rows, int lane,
                                          float rs, uint8_t* stage) {
   const int q = lane & 3;
-  uint8_t* my_row = stage + lane * kStageRowBytes;
 #pragma unroll 1
-  for (int rel = 0; rel < Cols<MODE>::n; rel += kOutChunk) {
-    if (w.col + rel >= p.out_cols) break;
-    uint32_t packed[16];
-    out_chunk<MODE>(p, w, tacc, rel, rs, stage, packed);
-    __syncwarp();
+  for (int rel = 0; rel < Cols<MODE>::n; rel += 16) {
+    if (w.col + (rel & ~(kOutChunk - 1)) >= p.out_cols) break;
+    float h[16];
+    outputs<MODE, ACT>(p, w, tacc, rel, rs, stage, h);
+    const int c0 = (rel & 16) >> 3;  // first of the two pieces of the row
+    if (c0 == 0) __syncwarp();       // the block before is stored
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint4*>(my_row + 16 * c) =
-          make_uint4(packed[4 * c], packed[4 * c + 1], packed[4 * c + 2], packed[4 * c + 3]);
+    for (int c = 0; c < 2; ++c)
+      *reinterpret_cast<uint4*>(turned(stage, lane, c0 + c)) =
+          make_uint4(pack_bf16x2(h[8 * c], h[8 * c + 1]), pack_bf16x2(h[8 * c + 2], h[8 * c + 3]),
+                     pack_bf16x2(h[8 * c + 4], h[8 * c + 5]), pack_bf16x2(h[8 * c + 6], h[8 * c + 7]));
+    if (c0 == 0) continue;
     __syncwarp();
-    const int col = w.col + rel + 8 * q;
+    const int col = w.col + rel - 16 + 8 * q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int l = 8 * i + (lane >> 2);  // the lane whose row this is
       const int r = w.row0 + l;
       if (l < w.lanes && r < rows && col < p.out_cols)
         *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(row0) + r) * p.out_cols + col) =
-            *reinterpret_cast<const uint4*>(stage + l * kStageRowBytes + 16 * q);
+            *reinterpret_cast<const uint4*>(turned(stage, l, q));
     }
   }
 }
 
-template <int MODE>
+template <int MODE, int ACT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapAh,
-                     const __grid_constant__ CUtensorMap mapAf, const __grid_constant__ CUtensorMap mapB,
-                     const Int8Params p) {
+                     const __grid_constant__ CUtensorMap mapB, const Int8Params p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (by an offset, so that the compiler still knows it for shared memory)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   uint8_t* ctrl = smem + STAGES * STAGE_BYTES;
   const uint32_t full0 = smem_u32(ctrl);        // STAGES mbarriers
@@ -269,10 +214,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 128);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 132);
   int* bad_flag = reinterpret_cast<int*>(ctrl + 136);
-  int* s_off = reinterpret_cast<int*>(ctrl + CTRL_BYTES);
+  uint8_t* s_stage = ctrl + CTRL_BYTES;  // NUM_EPI_WARPS of kWarpStage
+  int* s_off = reinterpret_cast<int*>(s_stage + NUM_EPI_WARPS * kWarpStage);
   int* s_mt = s_off + (p.E + 1);
-  uint8_t* s_stage =
-      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_mt + p.E + 1) + 15) & ~uintptr_t(15));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -302,33 +246,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   for (int i = threadIdx.x; i <= p.E; i += NUM_THREADS) s_off[i] = p.offsets[i];
   __syncthreads();
-  if (warp == 0) {
-    // Validate the CSR and build the per-expert prefix of tile pieces.
-    const int per = (p.E + 31) / 32;
-    const int e0 = min(lane * per, p.E), e1 = min(e0 + per, p.E);
-    int local = 0;
-    bool bad = false;
-    for (int e = e0; e < e1; ++e) {
-      const int cnt = s_off[e + 1] - s_off[e];
-      if (cnt < 0 || s_off[e] < 0 || s_off[e + 1] > p.R) bad = true;
-      else local += (cnt + BM - 1) / BM;
-    }
-    int incl = local;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += y;
-    }
-    int run = incl - local;
-    for (int e = e0; e < e1; ++e) {
-      s_mt[e] = run;
-      const int cnt = s_off[e + 1] - s_off[e];
-      if (cnt > 0) run += (cnt + BM - 1) / BM;
-    }
-    if (lane == 31) s_mt[p.E] = incl;
-    if (lane == 0 && s_off[0] != 0) bad = true;
-    if (__any_sync(0xffffffffu, bad) && lane == 0) *bad_flag = 1;
-  }
+  if (warp == 0) build_pieces(s_off, s_mt, bad_flag, p.E, p.R, BM, lane);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -344,13 +262,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = true;
       for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
         const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
-        // rows of A to copy: all 128, or 64 of a tile of at most 64, or 16 of one
-        // of at most 16; the rest of the stage holds old rows, whose sums are
-        // not stored
-        const bool half = tc.rows <= HALF_ROWS, few = tc.rows <= FEW_ROWS;
-        const int a_rows = few ? FEW_ROWS : half ? HALF_ROWS : BM;
-        const CUtensorMap* ma = few ? &mapAf : half ? &mapAh : &mapA;
-        const uint32_t bytes = static_cast<uint32_t>(a_rows * BK + B_BYTES);
+        const bool half = tc.rows <= HALF_ROWS;
+        const CUtensorMap* ma = half ? &mapAh : &mapA;
+        const uint32_t bytes = half ? HALF_A_BYTES + B_BYTES : STAGE_BYTES;
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t ph = static_cast<uint32_t>(it / STAGES) & 1u;
@@ -388,7 +302,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       // ---------------------------------------------------- MMA issuer
-      int it = 0, ti = 0;
+      int s = 0, ti = 0;
+      uint32_t ph = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++ti) {
         const int acc = ti & 1;
@@ -400,22 +315,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
         const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
         const uint32_t idesc = tc.rows <= HALF_ROWS ? idesc_s8_s32(HALF_ROWS, BN) : idesc_s8_s32(BM, BN);
-        for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait(full0 + 8 * s, static_cast<uint32_t>(it / STAGES) & 1u, abort_flag, kTimeoutNs)) {
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!mbar_wait(full0 + 8 * s, ph, abort_flag, kTimeoutNs)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + A_BYTES;
-#pragma unroll
-          for (int kk = 0; kk < BK / UMMA_K; ++kk) {
-            // K-major rows of 128 B, 8-row swizzle atoms 1024 B apart; a
-            // 32-wide K step is 32 B along the row
-            mma_i8_ss(d_tmem, smem_desc_sw128(sa + kk * UMMA_K, 16, 1024),
-                      smem_desc_sw128(sb + kk * UMMA_K, 16, 1024), idesc, (kb | kk) != 0 ? 1u : 0u);
-          }
+          const uint32_t a_lo = desc_lo(sbase + s * STAGE_BYTES);
+          mma_i8_stage(d_tmem, a_lo, a_lo + A_BYTES / 16, idesc, kb == 0);
           mma_commit(empty0 + 8 * s);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
         if (!ok) break;
         mma_commit(tfull0 + 8 * acc);
@@ -442,7 +354,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after_sync();
       const uint32_t tacc = tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quad * 32) << 16);
-      epilogue<MODE>(p, w, tacc, tc.row0, tc.rows, lane, rs, stage);
+      epilogue<MODE, ACT>(p, w, tacc, tc.row0, tc.rows, lane, rs, stage);
       tc_fence_before_sync();
       mbar_arrive(tempty0 + 8 * acc);
     }
@@ -459,24 +371,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 constexpr size_t smem_bytes(int E) {
-  return 1024 + STAGES * STAGE_BYTES + CTRL_BYTES + 2 * static_cast<size_t>(E + 1) * 4 + 16 + NUM_EPI_WARPS * kWarpStage;
+  return 1024 + STAGES * STAGE_BYTES + CTRL_BYTES + NUM_EPI_WARPS * kWarpStage +
+         2 * static_cast<size_t>(E + 1) * 4;
 }
 
-template <int MODE>
+template <int MODE, int ACT>
 cudaError_t launch_mode(const Int8GemmArgs& a, cudaStream_t stream) {
   const bool down = MODE == MODE_DOWN;
   const int K = down ? a.D : a.H;
   const cuuint64_t pitch = static_cast<cuuint64_t>(int8_pitch(K));
   const cuuint64_t N = down ? a.H : 2 * static_cast<cuuint64_t>(a.D), E = a.E;
   constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  CUtensorMap mapA, mapAh, mapAf, mapB;
+  CUtensorMap mapA, mapAh, mapB;
   {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(a.R)};
     const cuuint64_t strides[1] = {pitch};
-    const cuuint32_t box[2] = {BK, BM}, half_box[2] = {BK, HALF_ROWS}, few_box[2] = {BK, FEW_ROWS};
+    const cuuint32_t box[2] = {BK, BM}, half_box[2] = {BK, HALF_ROWS};
     if (!encode_tiled_map(&mapA, kU8, a.A, 2, dims, strides, box) ||
-        !encode_tiled_map(&mapAh, kU8, a.A, 2, dims, strides, half_box) ||
-        !encode_tiled_map(&mapAf, kU8, a.A, 2, dims, strides, few_box))
+        !encode_tiled_map(&mapAh, kU8, a.A, 2, dims, strides, half_box))
       return cudaErrorInvalidValue;
   }
   if (MODE == MODE_CONCAT) {
@@ -491,38 +403,40 @@ cudaError_t launch_mode(const Int8GemmArgs& a, cudaStream_t stream) {
     const cuuint32_t box[3] = {BK, BN, 1};
     if (!encode_tiled_map(&mapB, kU8, a.W, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  Int8Params p;
-  p.offsets = a.offsets;
-  p.a_scales = a.a_scales;
-  p.w_scales = a.w_scales;
-  p.bias = a.bias;
-  p.out = a.out;
-  p.status = a.status;
-  p.E = a.E;
-  p.R = a.R;
-  p.N = static_cast<int>(N);
-  p.out_cols = down ? a.H : a.D;
+  Int8Params p = int8_params(a);
   p.n_tiles = (p.out_cols + (down ? BN : BN / 2) - 1) / (down ? BN : BN / 2);
   p.num_kb = (K + BK - 1) / BK;
-  p.activation = a.activation;
-  p.alpha = a.alpha;
-  p.limit = a.limit;
-  p.err_bit = down ? MOE_DEVICE_ERR_TIMEOUT_GEMM2 : MOE_DEVICE_ERR_TIMEOUT_GEMM1;
-  const void* kernel = reinterpret_cast<const void*>(int8_gemm_kernel<MODE>);
-  const cudaError_t err = opt_in_dynamic_smem(kernel, static_cast<int>(smem_bytes(kMaxExperts)));
+  const cudaError_t err = opt_in_dynamic_smem(reinterpret_cast<const void*>(int8_gemm_kernel<MODE, ACT>),
+                                              static_cast<int>(smem_bytes(kMaxExperts)));
   if (err != cudaSuccess) return err;
   const int64_t max_tiles = (static_cast<int64_t>(a.R) / BM + std::min(a.E, a.R)) * p.n_tiles;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(max_tiles, a.num_sms)));
-  return launch_pdl(int8_gemm_kernel<MODE>, grid, dim3(NUM_THREADS), smem_bytes(a.E), stream, mapA, mapAh, mapAf, mapB,
-                    p);
+  return launch_pdl(int8_gemm_kernel<MODE, ACT>, grid, dim3(NUM_THREADS), smem_bytes(a.E), stream, mapA, mapAh, mapB, p);
+}
+
+template <int MODE>
+cudaError_t launch_gate_up(const Int8GemmArgs& a, cudaStream_t stream) {
+  if (a.activation == MOE_ACT_SILU) return launch_mode<MODE, MOE_ACT_SILU>(a, stream);
+  if (a.activation == MOE_ACT_SWIGLUOAI) return launch_mode<MODE, MOE_ACT_SWIGLUOAI>(a, stream);
+  return launch_mode<MODE, MOE_ACT_GELU_TANH>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream) {
   if (a.R == 0) return cudaSuccess;
-  if (a.down) return launch_mode<MODE_DOWN>(a, stream);
-  return a.gate_up_format == 0 ? launch_mode<MODE_CONCAT>(a, stream) : launch_mode<MODE_INTERLEAVED>(a, stream);
+  // Few rows per expert go to the kernel with the operands exchanged
+  // (int8_few.cu): on one B200, 24 rows per expert (E 49, K 72, 13312 columns) 76 us
+  // here, 49 there; 2 rows (E 135, K 64) 117, 50; 64 rows (E 123, K 208) 226, 195;
+  // but 127 rows (E 18, K 344) 38, 47.  So it does where this one's 256-column tiles would leave
+  // half of the SMs idle, and it takes 128-column tiles (4 experts, 93 rows, K 6984:
+  // 36 us here, 26 there with 128 columns and 37 with 256).
+  const int64_t experts = std::min(a.E, a.R), columns = a.down ? a.H : 2 * static_cast<int64_t>(a.D);
+  const int64_t tiles = (a.R / BM + experts) * ((columns + BN - 1) / BN);
+  if (2 * tiles <= a.num_sms) return launch_int8_few(a, 128, stream);
+  if (a.R <= 64 * experts) return launch_int8_few(a, 256, stream);
+  if (a.down) return launch_mode<MODE_DOWN, MOE_ACT_SILU>(a, stream);  // (no activation)
+  return a.gate_up_format == 0 ? launch_gate_up<MODE_CONCAT>(a, stream) : launch_gate_up<MODE_INTERLEAVED>(a, stream);
 }
 
 }  // namespace moe

@@ -245,5 +245,7 @@ struct Int8GemmArgs {
   int num_sms;
 };
 cudaError_t launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream);
+// The same for few rows per expert, in tiles of wc weight columns (256 or 128).
+cudaError_t launch_int8_few(const Int8GemmArgs& a, int wc, cudaStream_t stream);
 
 }  // namespace moe

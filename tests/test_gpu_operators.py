@@ -458,7 +458,8 @@ def int8_case(T, H, D, E, k, part, fmt="concatenated", act="silu", bias=False, d
 INT8 = [  # T, H, D, E, k, drop, all on one expert
     (1, 8, 8, 1, 1, 0.0, None), (1, 264, 136, 8, 2, 0.0, None), (64, 128, 128, 1, 1, 0.0, 0), (65, 144, 256, 2, 1, 0.0, 1),
     (128, 392, 264, 3, 2, 0.0, 0), (129, 256, 128, 4, 1, 0.3, 2), (300, 520, 200, 40, 6, 0.1, None), (33, 1000, 96, 5, 3, 1.0, None),
-    (700, 136, 72, 3, 2, 0.0, None),
+    (700, 136, 72, 3, 2, 0.0, None), (300, 264, 1048, 30, 2, 0.1, None), (31, 1544, 2056, 40, 3, 0.0, 7),
+    (1300, 2576, 2568, 5, 2, 0.1, 1), (2000, 3080, 1544, 3, 1, 0.0, 2), (900, 2312, 2600, 9, 1, 0.0, None),
 ]
 
 
@@ -471,10 +472,32 @@ def test_grouped_linear_int8(T, H, D, E, k, drop, one, part):
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("fmt", ["concatenated", "interleaved"])
 @pytest.mark.parametrize("act,limit", [("silu", 0.0), ("silu", 1.5), ("swigluoai", 7.0), ("swigluoai", 0.0), ("gelu_tanh", 0.0)])
-def test_grouped_linear_int8_activations(act, limit, fmt, bias):
-    int8_case(150, 264, 328, 6, 2, "gate_up", fmt=fmt, act=act, limit=limit, bias=bias, seed=7)
+@pytest.mark.parametrize("T,H,D,E,k", [(150, 264, 328, 6, 2), (300, 264, 328, 40, 2), (1200, 264, 1288, 5, 1)],
+                         ids=["few_tiles", "few_rows", "many_rows"])
+def test_grouped_linear_int8_activations(T, H, D, E, k, act, limit, fmt, bias):
+    int8_case(T, H, D, E, k, "gate_up", fmt=fmt, act=act, limit=limit, bias=bias, seed=7)
     if act == "silu" and limit == 0:
-        int8_case(150, 264, 328, 6, 2, "down", fmt=fmt, bias=bias, seed=8)
+        int8_case(T, 8 * D, H, E, k, "down", fmt=fmt, bias=bias, seed=8)
+
+
+def test_grouped_linear_int8_same_bits_in_every_tile_shape():
+    """A row's product does not depend on how many rows its expert has, nor on the
+    kernel that takes them."""
+    H, D, E = 392, 1288, 4
+    g = torch.Generator().manual_seed(5)
+    w_q = torch.randint(-127, 128, (E, 2 * D, abi.int8_pitch(H)), generator=g, dtype=torch.int8).cuda()
+    w_s = (torch.rand(E, 2 * D, generator=g) * 0.002).cuda()
+    q = torch.randint(-127, 128, (2000, abi.int8_pitch(H)), generator=g, dtype=torch.int8).cuda()
+    s = (torch.rand(2000, generator=g) * 0.02).cuda()
+    outs = []
+    for T in (2000, 60, 5):
+        cfg = abi.config(T, H, E, 1, D, activation="swigluoai", alpha=R.ALPHA, limit=R.LIMIT)
+        out = torch.zeros(T, D, dtype=BF16, device="cuda")
+        ws = torch.empty(abi.moe_operator_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+        off = torch.tensor([0, T, T, T, T], dtype=torch.int32, device="cuda")   # all rows to expert 0
+        abi.moe_grouped_linear_int8(cfg, "gate_up", q[:T], s[:T], w_q, w_s, off, out, ws)
+        outs.append(out)
+    assert torch.equal(outs[0][:60], outs[1]) and torch.equal(outs[0][:5], outs[2])
 
 
 def test_grouped_linear_int8_largest_sums():
