@@ -13,8 +13,9 @@
 // What bounds it, on one B200 (6.56 TB/s copy rate): the weights' stream (E 128,
 // 2880 x 5760, 8192 rows in 344 us, 6.4 TB/s; E 64, 1536 x 4096, 256 rows in 54.6
 // us, of which 5 pass before the first copies have landed and 1.4 are the seventh
-// wave of 6.8; one token to 8 of those experts 12.7 us); with few tiles the chain
-// of stages in one SM, 0.27 us for 128 columns by 128 of K and 0.4 for 256.
+// wave of 6.8; one token to 8 of those experts 12.8 us); with few tiles the chain
+// of stages in one SM, 0.27 us for 128 columns by 128 of K and 0.4 for 256; with a
+// short K the epilogue's latency, 1.2 us for a tile of 2 rows and K 64.
 //
 // For gate_up a gate and its up column have to meet in one warp: interleaved
 // columns are neighbours, and concatenated ones are copied in groups of 8 gate
@@ -222,30 +223,51 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int wrow = block * MMA_COLS + quad * 32 + lane;  // this lane's weight column within the tile
     constexpr int kMate = MODE == MODE_CONCAT ? 8 : 1;  // lanes between a gate and its up column
     const bool is_up = MODE != MODE_DOWN && (lane & kMate) != 0;
+    // What a tile's epilogue needs from memory: fetched a tile ahead, since the
+    // scales come from HBM and a tile of few rows takes less than their latency.
+    struct Ahead {
+      TileCoord tc;
+      int col;               // this lane's output column
+      float ws, bias;        // and its column of W's
+      float rs[BR / 32];     // scales of rows lane, lane + 32, ...
+    };
+    auto fetch = [&](int t) {
+      Ahead f;
+      f.tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+      int wcol;
+      if constexpr (MODE == MODE_CONCAT) {
+        f.col = f.tc.n * (p.wc / 2) + (wrow >> 4) * 8 + (wrow & 7);
+        wcol = (is_up ? p.g.out_cols : 0) + f.col;
+      } else {
+        wcol = f.tc.n * p.wc + wrow;
+        f.col = MODE == MODE_INTERLEAVED ? wcol >> 1 : wcol;
+      }
+      f.ws = f.bias = 0.f;
+      if (f.col < p.g.out_cols) {
+        const int64_t at = static_cast<int64_t>(f.tc.e) * p.g.N + wcol;
+        f.ws = __ldg(p.g.w_scales + at);
+        if (p.g.bias != nullptr) f.bias = __bfloat162float(p.g.bias[at]);
+      }
+#pragma unroll
+      for (int i = 0; i < BR / 32; ++i) {
+        const int r = lane + 32 * i;
+        f.rs[i] = r < f.tc.rows ? __ldg(p.g.a_scales + f.tc.row0 + r) : 0.f;
+      }
+      return f;
+    };
+    Ahead next = {};
+    if (static_cast<int>(blockIdx.x) < total) next = fetch(blockIdx.x);
     int ti = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
-      const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
-      const int acc = ti & 1;
-      // output column, and column of W, of this lane
-      int col, wcol;
-      if constexpr (MODE == MODE_CONCAT) {
-        col = tc.n * (p.wc / 2) + (wrow >> 4) * 8 + (wrow & 7);
-        wcol = (is_up ? p.g.out_cols : 0) + col;
-      } else {
-        wcol = tc.n * p.wc + wrow;
-        col = MODE == MODE_INTERLEAVED ? wcol >> 1 : wcol;
-      }
+      const TileCoord tc = next.tc;
+      const int acc = ti & 1, col = next.col;
+      const float ws = next.ws, bias = next.bias;
       const bool in = col < p.g.out_cols;
-      float ws = 0.f, bias = 0.f;
-      if (in) {
-        const int64_t at = static_cast<int64_t>(tc.e) * p.g.N + wcol;
-        ws = __ldg(p.g.w_scales + at);
-        if (p.g.bias != nullptr) bias = __bfloat162float(p.g.bias[at]);
-      }
       __syncwarp();  // every lane is done with the tile before
-      for (int r = lane; r < ((tc.rows + 15) & ~15); r += 32)
-        scales[r] = r < tc.rows ? __ldg(p.g.a_scales + tc.row0 + r) : 0.f;
+#pragma unroll
+      for (int i = 0; i < BR / 32; ++i) scales[lane + 32 * i] = next.rs[i];
       __syncwarp();
+      if (t + static_cast<int>(gridDim.x) < total) next = fetch(t + gridDim.x);
       const bool got = mbar_wait(tfull0 + 8 * acc, static_cast<uint32_t>(ti >> 1) & 1u, abort_flag, kTimeoutNs);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after_sync();

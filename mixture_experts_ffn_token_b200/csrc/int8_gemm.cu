@@ -82,31 +82,40 @@ __device__ __forceinline__ uint8_t* turned(uint8_t* stage, int r, int c) {
   return stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// The scales and biases are fetched in groups of four columns, one a lane, while
-// the tile's product is still running, since they come from HBM.
-// Concatenated: the gate columns' groups, then the up columns'.
+// What a tile's epilogue needs from memory, fetched a tile ahead, since it comes
+// from HBM: the scales and biases in groups of four columns, one a lane
+// (concatenated: the gate columns' groups, then the up columns').
 
+struct Ahead {
+  TileCoord tc;
+  Part w;
+  float rs;   // the scale of this lane's row
+  float4 s;   // this lane's group
+  uint2 b;
+};
 template <int MODE>
-__device__ __forceinline__ void stage_columns(const Int8Params& p, const Part& w, int e, int lane, uint8_t* stage) {
+__device__ __forceinline__ Ahead fetch(const Int8Params& p, int t, const int* s_mt, const int* s_off, int quad, int part,
+                                       int lane) {
+  Ahead f;
+  f.tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
+  f.w = warp_part<MODE>(f.tc.n, quad, part, f.tc.rows <= HALF_ROWS);
+  f.rs = lane < f.w.lanes && f.w.row0 + lane < f.tc.rows ? __ldg(p.a_scales + f.tc.row0 + f.w.row0 + lane) : 0.f;
   int c = -1;  // the group's first weight column, or -1 past the end
   if constexpr (MODE == MODE_CONCAT) {
-    const int h = w.col + 4 * (lane & 15);
+    const int h = f.w.col + 4 * (lane & 15);
     if (h < p.out_cols) c = (lane < 16 ? 0 : p.out_cols) + h;
   } else {
-    const int first = w.col * Cols<MODE>::PER + 4 * lane;
+    const int first = f.w.col * Cols<MODE>::PER + 4 * lane;
     if (first < p.N) c = first;
   }
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  uint2 b = make_uint2(0u, 0u);
+  f.s = make_float4(0.f, 0.f, 0.f, 0.f);
+  f.b = make_uint2(0u, 0u);
   if (c >= 0) {
-    const int64_t at = static_cast<int64_t>(e) * p.N + c;
-    s = __ldg(reinterpret_cast<const float4*>(p.w_scales + at));
-    if (p.bias != nullptr) b = __ldg(reinterpret_cast<const uint2*>(p.bias + at));
+    const int64_t at = static_cast<int64_t>(f.tc.e) * p.N + c;
+    f.s = __ldg(reinterpret_cast<const float4*>(p.w_scales + at));
+    if (p.bias != nullptr) f.b = __ldg(reinterpret_cast<const uint2*>(p.bias + at));
   }
-  __syncwarp();  // every lane is done with the tile before
-  *reinterpret_cast<float4*>(stage + kScalesAt + 16 * lane) = s;
-  *reinterpret_cast<uint2*>(stage + kBiasAt + 8 * lane) = b;
-  __syncwarp();
+  return f;
 }
 
 struct Col4 {
@@ -343,13 +352,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int quad = warp & 3;         // this warp may access TMEM lanes 32*quad..+31
     const int part = (warp - 2) >> 2;  // which half of the tile's columns
     uint8_t* stage = s_stage + (warp - 2) * kWarpStage;
+    Ahead next = {};
+    if (static_cast<int>(blockIdx.x) < total) next = fetch<MODE>(p, blockIdx.x, s_mt, s_off, quad, part, lane);
     int ti = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
-      const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
       const int acc = ti & 1;
-      const Part w = warp_part<MODE>(tc.n, quad, part, tc.rows <= HALF_ROWS);
-      const float rs = lane < w.lanes && w.row0 + lane < tc.rows ? __ldg(p.a_scales + tc.row0 + w.row0 + lane) : 0.f;
-      stage_columns<MODE>(p, w, tc.e, lane, stage);
+      const TileCoord tc = next.tc;
+      const Part w = next.w;
+      const float rs = next.rs;
+      __syncwarp();  // every lane is done with the tile before
+      *reinterpret_cast<float4*>(stage + kScalesAt + 16 * lane) = next.s;
+      *reinterpret_cast<uint2*>(stage + kBiasAt + 8 * lane) = next.b;
+      __syncwarp();
+      if (t + static_cast<int>(gridDim.x) < total)
+        next = fetch<MODE>(p, t + gridDim.x, s_mt, s_off, quad, part, lane);
       const bool got = mbar_wait(tfull0 + 8 * acc, static_cast<uint32_t>(ti >> 1) & 1u, abort_flag, kTimeoutNs);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after_sync();
@@ -426,15 +442,15 @@ cudaError_t launch_gate_up(const Int8GemmArgs& a, cudaStream_t stream) {
 cudaError_t launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream) {
   if (a.R == 0) return cudaSuccess;
   // Few rows per expert go to the kernel with the operands exchanged
-  // (int8_few.cu): on one B200, 24 rows per expert (E 49, K 72, 13312 columns) 76 us
-  // here, 49 there; 2 rows (E 135, K 64) 117, 50; 64 rows (E 123, K 208) 226, 195;
-  // but 127 rows (E 18, K 344) 38, 47.  So it does where this one's 256-column tiles would leave
-  // half of the SMs idle, and it takes 128-column tiles (4 experts, 93 rows, K 6984:
-  // 36 us here, 26 there with 128 columns and 37 with 256).
+  // (int8_few.cu): on one B200, 2 rows per expert (E 135, K 64, 8848 columns) 117 us
+  // here, 41 there; 24 rows (E 49, K 72) 76, 44; 64 rows (E 123, K 208) 222, 195; 96
+  // rows (E 128, K 2048) 78, 80; 127 rows (E 18, K 344) 38, 47.  So does what this
+  // one's 256-column tiles would leave half of the SMs idle with, in 128-column
+  // tiles (4 experts, 93 rows, K 6984: 36 us here, 37 there, 26 with 128 columns).
   const int64_t experts = std::min(a.E, a.R), columns = a.down ? a.H : 2 * static_cast<int64_t>(a.D);
   const int64_t tiles = (a.R / BM + experts) * ((columns + BN - 1) / BN);
   if (2 * tiles <= a.num_sms) return launch_int8_few(a, 128, stream);
-  if (a.R <= 64 * experts) return launch_int8_few(a, 256, stream);
+  if (a.R <= 80 * experts) return launch_int8_few(a, 256, stream);
   if (a.down) return launch_mode<MODE_DOWN, MOE_ACT_SILU>(a, stream);  // (no activation)
   return a.gate_up_format == 0 ? launch_gate_up<MODE_CONCAT>(a, stream) : launch_gate_up<MODE_INTERLEAVED>(a, stream);
 }
