@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = true;
       for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
         const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
-        // the smallest box that holds the rows (at most pt, itself a box)
+        // the smallest box that holds the rows
         const int rows = tc.rows <= 16 ? 16 : tc.rows <= 32 ? 32 : tc.rows <= 64 ? 64 : 128;
         const CUtensorMap* ma = rows == 16 ? &mapA16 : rows == 32 ? &mapA32 : rows == 64 ? &mapA64 : &mapA128;
         for (int kb = 0; kb < p.g.num_kb; ++kb, ++it) {
