@@ -37,7 +37,8 @@ constexpr int NUM_EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + 32 * NUM_EPI_WARPS;
 constexpr int CTRL_BYTES = 512;
 constexpr int RING_BYTES = 192 * 1024;
-constexpr int MAX_STAGES = 6;
+constexpr int MAX_STAGES = 10;
+constexpr int AHEAD_BYTES = 128 * 1024;
 constexpr int BR = 128;                     // rows of a tile
 constexpr int MMA_COLS = 128;               // weight columns of an MMA (its M)
 constexpr uint32_t TMEM_COLS = 2 * 2 * BR;  // two accumulators of at most two MMAs
@@ -46,7 +47,9 @@ struct FewParams {
   Int8Params g;
   int wc;       // weight columns of a tile
   int blocks;   // MMAs across them
+  int cap;      // rows of a stage: 16, 32, 64 or 128, whatever holds a tile's
   int stages;
+  int ahead;    // weight boxes fetched to L2 before the kernels before are done
 };
 
 // Stores v[0..N) -- this lane's column at N rows, the rows of two lanes `d`
@@ -110,13 +113,37 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
+  // While the kernels before (as a rule the rows' quantiser) still run, the first
+  // tile's weights are fetched to L2, where their copies then find them: a hint,
+  // which cannot make a value stale.  The offsets that it goes by may still be
+  // changing, so it takes any CSR, and they are read again afterwards.
+  __syncthreads();
+  for (int i = threadIdx.x; i <= p.g.E; i += NUM_THREADS) s_off[i] = __ldcg(p.g.offsets + i);
+  __syncthreads();
+  if (warp == 0) {
+    build_pieces(s_off, s_mt, bad_flag, p.g.E, p.g.R, BR, lane);
+    __syncwarp();
+    const int t = blockIdx.x;
+    if (*bad_flag == 0 && t < s_mt[p.g.E] * p.g.n_tiles) {
+      const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+      for (int kb = lane; kb < p.ahead; kb += 32) {
+        if constexpr (MODE == MODE_CONCAT) tma_prefetch_5d(&mapB, kb * BK, 0, 0, tc.n * (p.wc / 16), tc.e);
+        else tma_prefetch_3d(&mapB, kb * BK, tc.n * p.wc, tc.e);
+      }
+    }
+  }
   griddep_wait();  // the offsets and operands of the kernels before are complete and visible
   // the status word of this call starts at zero: only this CTA records a bad
   // CSR, and a timed-out wait of another comes seconds later
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.g.status = 0;
-  for (int i = threadIdx.x; i <= p.g.E; i += NUM_THREADS) s_off[i] = p.g.offsets[i];
-  __syncthreads();
-  if (warp == 0) build_pieces(s_off, s_mt, bad_flag, p.g.E, p.g.R, BR, lane);
+  bool same = true;
+  for (int i = threadIdx.x; i <= p.g.E; i += NUM_THREADS) same = same && s_off[i] == __ldcg(p.g.offsets + i);
+  if (!__syncthreads_and(same)) {
+    for (int i = threadIdx.x; i <= p.g.E; i += NUM_THREADS) s_off[i] = __ldcg(p.g.offsets + i);
+    if (threadIdx.x == 0) *bad_flag = 0;
+    __syncthreads();
+    if (warp == 0) build_pieces(s_off, s_mt, bad_flag, p.g.E, p.g.R, BR, lane);
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -124,7 +151,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const bool bad = *bad_flag != 0;
   if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.g.status, MOE_DEVICE_ERR_CSR);
   const int total = bad ? 0 : s_mt[p.g.E] * p.g.n_tiles;
-  const int w_bytes = p.wc * BK, stage_bytes = w_bytes + BR * BK;
+  const int w_bytes = p.wc * BK, stage_bytes = w_bytes + p.cap * BK;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -361,7 +388,10 @@ cudaError_t launch_mode(const Int8GemmArgs& a, int wc, cudaStream_t stream) {
   p.g.num_kb = (K + BK - 1) / BK;
   p.wc = wc;
   p.blocks = wc / MMA_COLS;
-  p.stages = RING_BYTES / ((wc + BR) * BK);
+  // a tile has at most R rows: one token's few rows leave room for more stages
+  p.cap = a.R <= 16 ? 16 : a.R <= 32 ? 32 : a.R <= 64 ? 64 : BR;
+  p.stages = std::min(MAX_STAGES, RING_BYTES / ((wc + p.cap) * BK));
+  p.ahead = std::min(p.g.num_kb, AHEAD_BYTES / (wc * BK));
   const cudaError_t err = opt_in_dynamic_smem(reinterpret_cast<const void*>(int8_few_kernel<MODE, ACT>),
                                               static_cast<int>(smem_bytes(kMaxExperts)));
   if (err != cudaSuccess) return err;
