@@ -153,94 +153,105 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int total = bad ? 0 : s_mt[p.g.E] * p.g.n_tiles;
   const int w_bytes = p.wc * BK, stage_bytes = w_bytes + p.cap * BK;
 
+  // Both single-thread roles run as whole warps of which one lane issues: then
+  // the loops' values are uniform.
   if (warp == 0) {
-    if (lane == 0) {
-      // -------------------------------------------------- TMA producer
-      int it = 0, s = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
-        // the smallest box that holds the rows
-        const int rows = tc.rows <= 16 ? 16 : tc.rows <= 32 ? 32 : tc.rows <= 64 ? 64 : 128;
-        const CUtensorMap* ma = rows == 16 ? &mapA16 : rows == 32 ? &mapA32 : rows == 64 ? &mapA64 : &mapA128;
-        for (int kb = 0; kb < p.g.num_kb; ++kb, ++it) {
-          if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, kTimeoutNs)) {
-            ok = false;
-            break;
-          }
+    // ---------------------------------------------------- TMA producer
+    int it = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const bool leader = elect_one();
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+      // the smallest box that holds the rows
+      const int rows = tc.rows <= 16 ? 16 : tc.rows <= 32 ? 32 : tc.rows <= 64 ? 64 : 128;
+      const CUtensorMap* ma = rows == 16 ? &mapA16 : rows == 32 ? &mapA32 : rows == 64 ? &mapA64 : &mapA128;
+      const uint32_t bytes = static_cast<uint32_t>(w_bytes + rows * BK);
+      for (int kb = 0; kb < p.g.num_kb; ++kb, ++it) {
+        if (!__all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, kTimeoutNs))) {
+          ok = false;
+          break;
+        }
+        if (leader) {
           const uint32_t sw = sbase + s * stage_bytes, fb = full0 + 8 * s;
-          mbar_arrive_expect_tx(fb, static_cast<uint32_t>(w_bytes + rows * BK));
+          mbar_arrive_expect_tx(fb, bytes);
           if constexpr (MODE == MODE_CONCAT) tma_load_5d(sw, &mapB, fb, kb * BK, 0, 0, tc.n * (p.wc / 16), tc.e);
           else tma_load_3d(sw, &mapB, fb, kb * BK, tc.n * p.wc, tc.e);
           tma_load_2d(sw + w_bytes, ma, fb, kb * BK, tc.row0);
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1u;
-          }
         }
-      }
-      if (ok) {
-        // wait until the MMAs have released every stage, so that no commit
-        // arrival lands after this CTA exits
-        for (int i = 0; i < p.stages; ++i) {
-          if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, kTimeoutNs)) break;
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-      } else {
-        // aborted: let the copies already issued land before shared memory is
-        // released (time-bounded, independent of the abort flag)
-        for (int i = 0; i < p.stages; ++i) {
-          if (it > i) {
-            const int last = i + ((it - 1 - i) / p.stages) * p.stages;
-            wait_time_only(full0 + 8 * i, static_cast<uint32_t>(last / p.stages) & 1u);
-          }
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1u;
         }
       }
     }
+    if (ok) {
+      // wait until the MMAs have released every stage, so that no commit
+      // arrival lands after this CTA exits
+      for (int i = 0; i < p.stages; ++i) {
+        if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, kTimeoutNs)) break;
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    } else {
+      // aborted: let the copies already issued land before shared memory is
+      // released (time-bounded, independent of the abort flag)
+      for (int i = 0; i < p.stages; ++i) {
+        if (it > i) {
+          const int last = i + ((it - 1 - i) / p.stages) * p.stages;
+          wait_time_only(full0 + 8 * i, static_cast<uint32_t>(last / p.stages) & 1u);
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------- MMA issuer
-      int s = 0, ti = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++ti) {
-        const int acc = ti & 1;
-        if (!mbar_wait(tempty0 + 8 * acc, (static_cast<uint32_t>(ti >> 1) & 1u) ^ 1u, abort_flag, kTimeoutNs)) {
+    // ------------------------------------------------------ MMA issuer
+    int s = 0, ti = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const bool leader = elect_one();
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++ti) {
+      const int acc = ti & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * acc, (static_cast<uint32_t>(ti >> 1) & 1u) ^ 1u, abort_flag,
+                                             kTimeoutNs))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 2 * BR);
+      const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+      const uint32_t idesc = idesc_s8_s32(MMA_COLS, (tc.rows + 15) & ~15);
+      for (int kb = 0; kb < p.g.num_kb; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, ph, abort_flag, kTimeoutNs))) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 2 * BR);
-        const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
-        const uint32_t idesc = idesc_s8_s32(MMA_COLS, (tc.rows + 15) & ~15);
-        for (int kb = 0; kb < p.g.num_kb; ++kb) {
-          if (!mbar_wait(full0 + 8 * s, ph, abort_flag, kTimeoutNs)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
+        if (leader) {
           const uint32_t w_lo = desc_lo(sbase + s * stage_bytes), r_lo = w_lo + (w_bytes >> 4);
           mma_i8_stage(d_tmem, w_lo, r_lo, idesc, kb == 0);
           if (p.blocks == 2) mma_i8_stage(d_tmem + BR, w_lo + MMA_COLS * BK / 16, r_lo, idesc, kb == 0);
           mma_commit(empty0 + 8 * s);
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1u;
-          }
         }
-        if (!ok) break;
-        mma_commit(tfull0 + 8 * acc);
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      if (!ok) {
-        // aborted: every MMA issued so far must finish before TMEM is freed
-        mma_commit(drain_bar);
-        wait_time_only(drain_bar, 0);
-      }
+      if (!ok) break;
+      if (leader) mma_commit(tfull0 + 8 * acc);
+      __syncwarp();
     }
+    if (!ok && leader) {
+      // aborted: every MMA issued so far must finish before TMEM is freed
+      mma_commit(drain_bar);
+      wait_time_only(drain_bar, 0);
+    }
+    __syncwarp();
   } else {
     // -------------------------------------------------------- epilogue
     const int quad = warp & 3;         // this warp may access TMEM lanes 32*quad..+31
