@@ -309,44 +309,52 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------- MMA issuer
-      int s = 0, ti = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++ti) {
-        const int acc = ti & 1;
-        if (!mbar_wait(tempty0 + 8 * acc, (static_cast<uint32_t>(ti >> 1) & 1u) ^ 1u, abort_flag, kTimeoutNs)) {
+    // ------------------------------------------------------ MMA issuer
+    // (a whole warp of which one lane issues: then the loop's values are uniform,
+    // and an MMA costs the thread no 40 cycles: E 8, 4096 x 28672, 8192 rows 827 ->
+    // 800 us; the copying warp likewise makes a short K slower, 75.6 -> 77.6)
+    int s = 0, ti = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const bool leader = elect_one();
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++ti) {
+      const int acc = ti & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * acc, (static_cast<uint32_t>(ti >> 1) & 1u) ^ 1u, abort_flag,
+                                             kTimeoutNs))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+      const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
+      const uint32_t idesc = tc.rows <= HALF_ROWS ? idesc_s8_s32(HALF_ROWS, BN) : idesc_s8_s32(BM, BN);
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, ph, abort_flag, kTimeoutNs))) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-        const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
-        const uint32_t idesc = tc.rows <= HALF_ROWS ? idesc_s8_s32(HALF_ROWS, BN) : idesc_s8_s32(BM, BN);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!mbar_wait(full0 + 8 * s, ph, abort_flag, kTimeoutNs)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
+        if (leader) {
           const uint32_t a_lo = desc_lo(sbase + s * STAGE_BYTES);
           mma_i8_stage(d_tmem, a_lo, a_lo + A_BYTES / 16, idesc, kb == 0);
           mma_commit(empty0 + 8 * s);
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
         }
-        if (!ok) break;
-        mma_commit(tfull0 + 8 * acc);
+        __syncwarp();
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      if (!ok) {
-        // aborted: every MMA issued so far must finish before TMEM is freed
-        mma_commit(drain_bar);
-        wait_time_only(drain_bar, 0);
-      }
+      if (!ok) break;
+      if (leader) mma_commit(tfull0 + 8 * acc);
+      __syncwarp();
     }
+    if (!ok && leader) {
+      // aborted: every MMA issued so far must finish before TMEM is freed
+      mma_commit(drain_bar);
+      wait_time_only(drain_bar, 0);
+    }
+    __syncwarp();
   } else {
     // -------------------------------------------------------- epilogue
     const int quad = warp & 3;         // this warp may access TMEM lanes 32*quad..+31
