@@ -49,6 +49,7 @@ struct FewParams {
   int blocks;   // MMAs across them
   int cap;      // rows of a stage: 16, 32, 64 or 128, whatever holds a tile's
   int stages;
+  int split;    // CTAs of a cluster that share a tile's K
   int ahead;    // weight boxes fetched to L2 before the kernels before are done
 };
 
@@ -68,7 +69,46 @@ __device__ __forceinline__ void store_pairs(const float (&v)[N], bool odd, int d
   }
 }
 
+// 16 rows of a tile, from their integer sums: `scales` holds the rows' and `ws`
+// this lane's column's, `out` is the first row's, `left` how many rows there are.
 template <int MODE, int ACT>
+__device__ __forceinline__ void finish_rows(const Int8Params& g, const uint32_t (&a)[16], const float* scales, float ws,
+                                            float bias, int lane, __nv_bfloat16* out, int col, int left) {
+  constexpr int kMate = MODE == MODE_CONCAT ? 8 : 1;  // lanes between a gate and its up column
+  const bool is_up = MODE != MODE_DOWN && (lane & kMate) != 0;
+  const bool in = col < g.out_cols;
+  const int64_t stride = g.out_cols;
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 rs = *reinterpret_cast<const float4*>(scales + i);
+    v[i] = int8_scaled(a[i], rs.x, ws, bias);
+    v[i + 1] = int8_scaled(a[i + 1], rs.y, ws, bias);
+    v[i + 2] = int8_scaled(a[i + 2], rs.z, ws, bias);
+    v[i + 3] = int8_scaled(a[i + 3], rs.w, ws, bias);
+  }
+  if constexpr (MODE == MODE_DOWN) {
+    store_pairs(v, (lane & 1) != 0, 1, out, stride, col, in, [&](int i) { return i < left ? i : -1; });
+  } else {
+    float h[8];  // of rows 2i (gate lane) or 2i + 1 (up lane)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, is_up ? v[2 * i] : v[2 * i + 1], kMate);
+      h[i] = is_up ? gated<ACT>(other, v[2 * i + 1], g.alpha, g.limit) : gated<ACT>(v[2 * i], other, g.alpha, g.limit);
+    }
+    constexpr int kNext = MODE == MODE_CONCAT ? 1 : 2;  // lanes between neighbouring h columns
+    store_pairs(h, (lane & kNext) != 0, kNext, out, stride, col, in, [&](int i) {
+      const int r = 2 * i + (is_up ? 1 : 0);
+      return r < left ? r : -1;
+    });
+  }
+}
+
+// SPLIT: a cluster of `split` CTAs shares each tile's K, one tile a cluster (128
+// columns).  Each leaves its integer sums in shared memory, in the ring that is
+// then done with, and CTA q finishes every split-th 16 rows from q on with the
+// sums of all: they are whole numbers, so the results are the same bits.
+template <int MODE, int ACT, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     int8_few_kernel(const __grid_constant__ CUtensorMap mapA16, const __grid_constant__ CUtensorMap mapA32,
                     const __grid_constant__ CUtensorMap mapA64, const __grid_constant__ CUtensorMap mapA128,
@@ -92,6 +132,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   int* s_mt = s_off + (p.g.E + 1);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  // this CTA's tiles and its part of their K
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = SPLIT ? static_cast<int>(blockIdx.x) / p.split : static_cast<int>(blockIdx.x);
+  const int step = SPLIT ? static_cast<int>(gridDim.x) / p.split : static_cast<int>(gridDim.x);
+  const int kb0 = SPLIT ? p.g.num_kb * rank / p.split : 0;
+  const int kb1 = SPLIT ? p.g.num_kb * (rank + 1) / p.split : p.g.num_kb;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -123,10 +169,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0) {
     build_pieces(s_off, s_mt, bad_flag, p.g.E, p.g.R, BR, lane);
     __syncwarp();
-    const int t = blockIdx.x;
+    const int t = first;
     if (*bad_flag == 0 && t < s_mt[p.g.E] * p.g.n_tiles) {
       const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
-      for (int kb = lane; kb < p.ahead; kb += 32) {
+      for (int kb = kb0 + lane; kb < min(kb1, kb0 + p.ahead); kb += 32) {
         if constexpr (MODE == MODE_CONCAT) tma_prefetch_5d(&mapB, kb * BK, 0, 0, tc.n * (p.wc / 16), tc.e);
         else tma_prefetch_3d(&mapB, kb * BK, tc.n * p.wc, tc.e);
       }
@@ -161,13 +207,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t ph = 0;
     bool ok = true;
     const bool leader = elect_one();
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+    for (int t = first; ok && t < total; t += step) {
       const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
       // the smallest box that holds the rows
       const int rows = tc.rows <= 16 ? 16 : tc.rows <= 32 ? 32 : tc.rows <= 64 ? 64 : 128;
       const CUtensorMap* ma = rows == 16 ? &mapA16 : rows == 32 ? &mapA32 : rows == 64 ? &mapA64 : &mapA128;
       const uint32_t bytes = static_cast<uint32_t>(w_bytes + rows * BK);
-      for (int kb = 0; kb < p.g.num_kb; ++kb, ++it) {
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
         if (!__all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, kTimeoutNs))) {
           ok = false;
           break;
@@ -213,7 +259,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t ph = 0;
     bool ok = true;
     const bool leader = elect_one();
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++ti) {
+    for (int t = first; ok && t < total; t += step, ++ti) {
       const int acc = ti & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * acc, (static_cast<uint32_t>(ti >> 1) & 1u) ^ 1u, abort_flag,
                                              kTimeoutNs))) {
@@ -224,7 +270,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 2 * BR);
       const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
       const uint32_t idesc = idesc_s8_s32(MMA_COLS, (tc.rows + 15) & ~15);
-      for (int kb = 0; kb < p.g.num_kb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, ph, abort_flag, kTimeoutNs))) {
           ok = false;
           break;
@@ -232,8 +278,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after_sync();
         if (leader) {
           const uint32_t w_lo = desc_lo(sbase + s * stage_bytes), r_lo = w_lo + (w_bytes >> 4);
-          mma_i8_stage(d_tmem, w_lo, r_lo, idesc, kb == 0);
-          if (p.blocks == 2) mma_i8_stage(d_tmem + BR, w_lo + MMA_COLS * BK / 16, r_lo, idesc, kb == 0);
+          mma_i8_stage(d_tmem, w_lo, r_lo, idesc, kb == kb0);
+          if (p.blocks == 2) mma_i8_stage(d_tmem + BR, w_lo + MMA_COLS * BK / 16, r_lo, idesc, kb == kb0);
           mma_commit(empty0 + 8 * s);
         }
         __syncwarp();
@@ -252,8 +298,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       wait_time_only(drain_bar, 0);
     }
     __syncwarp();
-  } else {
-    // -------------------------------------------------------- epilogue
+  }
+
+  // ---------------------------------------------------------- epilogue
+  if (warp >= 2) {
     const int quad = warp & 3;         // this warp may access TMEM lanes 32*quad..+31
     const int part = (warp - 2) >> 2;  // two blocks: the block; one: every other 16 rows
     float* scales = s_scales + (warp - 2) * BR;
@@ -294,64 +342,98 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       return f;
     };
     Ahead next = {};
-    if (static_cast<int>(blockIdx.x) < total) next = fetch(blockIdx.x);
+    if (first < total) next = fetch(first);
+    if constexpr (SPLIT) {
+      const TileCoord tc = next.tc;
+#pragma unroll
+      for (int i = 0; i < BR / 32; ++i) scales[lane + 32 * i] = next.rs[i];
+      __syncwarp();
+      const bool got = first < total && __all_sync(0xffffffffu, mbar_wait(tfull0, 0, abort_flag, kTimeoutNs));
+      tc_fence_after_sync();
+      const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+      // rows r0 .. r0 + 15 of the CTAs' sums, four rows of a column together (the
+      // copies and products that used this memory are complete: tfull)
+      const uint32_t mine = sbase + static_cast<uint32_t>(quad * 32 + lane) * 16;
+      constexpr uint32_t kFour = MMA_COLS * 16;
+      if (got) {
+        for (int r0 = 16 * part; r0 < tc.rows; r0 += 32) {
+          if (((r0 >> 4) & (p.split - 1)) == rank) continue;
+          uint32_t a[16];
+          tmem_ld16(tacc + static_cast<uint32_t>(r0), a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            st_shared_v4(mine + (r0 / 4 + i) * kFour, make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
+        }
+      }
+      __syncwarp();
+      cluster_sync();
+      if (got) {
+        for (int r0 = 16 * part; r0 < tc.rows; r0 += 32) {
+          if (((r0 >> 4) & (p.split - 1)) != rank) continue;
+          uint32_t a[16];
+          tmem_ld16(tacc + static_cast<uint32_t>(r0), a);
+          tmem_ld_wait();
+          for (int q0 = 1; q0 < p.split; q0 += 4) {  // four CTAs' loads in flight
+            uint4 b[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t from = map_to_rank(mine, static_cast<uint32_t>((rank + q0 + j) & (p.split - 1)));
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                b[j][i] = q0 + j < p.split ? ld_cluster_v4(from + (r0 / 4 + i) * kFour) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                a[4 * i] += b[j][i].x;
+                a[4 * i + 1] += b[j][i].y;
+                a[4 * i + 2] += b[j][i].z;
+                a[4 * i + 3] += b[j][i].w;
+              }
+          }
+          finish_rows<MODE, ACT>(p.g, a, scales + r0, next.ws, next.bias, lane,
+                                 p.g.out + (static_cast<int64_t>(tc.row0) + r0) * p.g.out_cols, next.col, tc.rows - r0);
+        }
+      }
+      tc_fence_before_sync();
+    }
     int ti = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
+    for (int t = first; !SPLIT && t < total; t += step, ++ti) {
       const TileCoord tc = next.tc;
       const int acc = ti & 1, col = next.col;
       const float ws = next.ws, bias = next.bias;
-      const bool in = col < p.g.out_cols;
       __syncwarp();  // every lane is done with the tile before
 #pragma unroll
       for (int i = 0; i < BR / 32; ++i) scales[lane + 32 * i] = next.rs[i];
       __syncwarp();
-      if (t + static_cast<int>(gridDim.x) < total) next = fetch(t + gridDim.x);
+      if (t + step < total) next = fetch(t + step);
       const bool got = mbar_wait(tfull0 + 8 * acc, static_cast<uint32_t>(ti >> 1) & 1u, abort_flag, kTimeoutNs);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after_sync();
       const uint32_t tacc = tmem_base + static_cast<uint32_t>((acc * 2 + block) * BR) +
                             (static_cast<uint32_t>(quad * 32) << 16);
       __nv_bfloat16* out = p.g.out + static_cast<int64_t>(tc.row0) * p.g.out_cols;
-      const int64_t stride = p.g.out_cols;
       const int r_step = p.blocks == 2 ? 16 : 32;
 #pragma unroll 1
       for (int r0 = p.blocks == 2 ? 0 : 16 * part; r0 < tc.rows; r0 += r_step) {
         uint32_t a[16];
         tmem_ld16(tacc + static_cast<uint32_t>(r0), a);
         tmem_ld_wait();
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 rs = *reinterpret_cast<const float4*>(scales + r0 + i);
-          v[i] = int8_scaled(a[i], rs.x, ws, bias);
-          v[i + 1] = int8_scaled(a[i + 1], rs.y, ws, bias);
-          v[i + 2] = int8_scaled(a[i + 2], rs.z, ws, bias);
-          v[i + 3] = int8_scaled(a[i + 3], rs.w, ws, bias);
-        }
-        const int left = tc.rows - r0;
-        if constexpr (MODE == MODE_DOWN) {
-          store_pairs(v, (lane & 1) != 0, 1, out + r0 * stride, stride, col, in,
-                      [&](int i) { return i < left ? i : -1; });
-        } else {
-          float h[8];  // of rows 2i (gate lane) or 2i + 1 (up lane)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float other = __shfl_xor_sync(0xffffffffu, is_up ? v[2 * i] : v[2 * i + 1], kMate);
-            h[i] = is_up ? gated<ACT>(other, v[2 * i + 1], p.g.alpha, p.g.limit)
-                         : gated<ACT>(v[2 * i], other, p.g.alpha, p.g.limit);
-          }
-          constexpr int kNext = MODE == MODE_CONCAT ? 1 : 2;  // lanes between neighbouring h columns
-          store_pairs(h, (lane & kNext) != 0, kNext, out + r0 * stride, stride, col, in, [&](int i) {
-            const int r = 2 * i + (is_up ? 1 : 0);
-            return r < left ? r : -1;
-          });
-        }
+        finish_rows<MODE, ACT>(p.g, a, scales + r0, ws, bias, lane, out + static_cast<int64_t>(r0) * p.g.out_cols, col,
+                               tc.rows - r0);
       }
       tc_fence_before_sync();
       mbar_arrive(tempty0 + 8 * acc);
     }
   }
 
+  __syncwarp();
+  if constexpr (SPLIT) {
+    if (warp < 2) cluster_sync();  // (the epilogue's, between leaving the sums and reading them)
+    cluster_sync();                // the others have read this CTA's sums
+  }
   __syncthreads();
   griddep_launch_dependents();  // this CTA has no tiles left: the next kernel may begin launching
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.g.status, p.g.err_bit);
@@ -364,6 +446,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 constexpr size_t smem_bytes(int E) {
   return 1024 + RING_BYTES + CTRL_BYTES + NUM_EPI_WARPS * BR * 4 + 2 * static_cast<size_t>(E + 1) * 4;
+}
+
+// K is split where the tiles leave SMs idle: by the largest power of two up to 8
+// that finds SMs for all (clusters of 4 and 8 fit within groups of SMs, so some
+// stay out) and leaves four stages to each.
+int k_split(int64_t tiles, int num_kb, int num_sms) {
+  int split = 1;
+  while (split < 8 && tiles * 2 * split <= (split == 1 ? num_sms : num_sms * 7 / 8) && num_kb >= 8 * split) split *= 2;
+  return split;
 }
 
 template <int MODE, int ACT>
@@ -403,13 +494,16 @@ cudaError_t launch_mode(const Int8GemmArgs& a, int wc, cudaStream_t stream) {
   p.cap = a.R <= 16 ? 16 : a.R <= 32 ? 32 : a.R <= 64 ? 64 : BR;
   p.stages = std::min(MAX_STAGES, RING_BYTES / ((wc + p.cap) * BK));
   p.ahead = std::min(p.g.num_kb, AHEAD_BYTES / (wc * BK));
-  const cudaError_t err = opt_in_dynamic_smem(reinterpret_cast<const void*>(int8_few_kernel<MODE, ACT>),
-                                              static_cast<int>(smem_bytes(kMaxExperts)));
-  if (err != cudaSuccess) return err;
   const int64_t max_tiles = (static_cast<int64_t>(a.R) / BR + std::min(a.E, a.R)) * p.g.n_tiles;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(max_tiles, a.num_sms)));
-  return launch_pdl(int8_few_kernel<MODE, ACT>, grid, dim3(NUM_THREADS), smem_bytes(a.E), stream, mapA[0], mapA[1],
-                    mapA[2], mapA[3], mapB, p);
+  p.split = wc == MMA_COLS ? k_split(max_tiles, p.g.num_kb, a.num_sms) : 1;
+  const auto kernel = p.split > 1 ? int8_few_kernel<MODE, ACT, true> : int8_few_kernel<MODE, ACT, false>;
+  const cudaError_t err =
+      opt_in_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem_bytes(kMaxExperts)));
+  if (err != cudaSuccess) return err;
+  // (a cluster has one tile at most)
+  const int64_t ctas = p.split > 1 ? max_tiles * p.split : std::min<int64_t>(max_tiles, a.num_sms);
+  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(ctas)), dim3(NUM_THREADS), p.split, smem_bytes(a.E), stream,
+                            mapA[0], mapA[1], mapA[2], mapA[3], mapB, p);
 }
 
 template <int MODE>

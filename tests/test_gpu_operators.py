@@ -480,6 +480,73 @@ def test_grouped_linear_int8_activations(T, H, D, E, k, act, limit, fmt, bias):
         int8_case(T, 8 * D, H, E, k, "down", fmt=fmt, bias=bias, seed=8)
 
 
+@pytest.mark.parametrize("K", [1016, 1032, 2184, 4104, 8200])
+@pytest.mark.parametrize("T,N,E,k,drop,one", [
+    (1, 128, 1, 1, 0.0, None), (17, 136, 2, 1, 0.0, None), (100, 264, 3, 2, 0.2, None), (128, 512, 4, 1, 0.0, 2),
+    (130, 128, 2, 1, 0.0, 0), (12, 1040, 5, 2, 1.0, None), (300, 520, 6, 1, 0.0, None)])
+def test_grouped_linear_int8_long_k_few_tiles(K, T, N, E, k, drop, one):
+    """A K that several blocks share: from two parts to eight, equal and not, with one
+    row and with two pieces, empty experts and no row at all."""
+    int8_case(T, N, K, E, k, "down", drop=drop, one=one, seed=11, bias=T % 2 == 1)
+    int8_case(T, K, N // 16 * 8, E, k, "gate_up", drop=drop, one=one, seed=12, fmt="concatenated" if T % 2 else "interleaved",
+              act="swigluoai", bias=T % 2 == 0)
+
+
+@pytest.mark.parametrize("part", ["gate_up", "down"])
+@pytest.mark.parametrize("rows", [1, 16, 31, 100, 128])
+def test_grouped_linear_int8_same_bits_however_k_is_shared(rows, part):
+    """The same rows and weights in batches of other sizes, which share K otherwise or not at all."""
+    K, N, E = 4104, 256, 2
+    H, D = (K, N // 2) if part == "gate_up" else (N, K)
+    g = torch.Generator().manual_seed(rows)
+    w_q = torch.randint(-127, 128, (E, N, abi.int8_pitch(K)), generator=g, dtype=torch.int8).cuda()
+    w_s = (torch.rand(E, N, generator=g) * 0.002).cuda()
+    q = torch.randint(-127, 128, (7000, abi.int8_pitch(K)), generator=g, dtype=torch.int8).cuda()
+    s = (torch.rand(7000, generator=g) * 0.02).cuda()
+    off = torch.tensor([0, 0, rows], dtype=torch.int32, device="cuda")
+    outs = []
+    for T in (rows, 600, 1400, 7000):  # 4, 12 (or 4), 24 and 112 tiles at most
+        cfg = abi.config(T, H, E, 1, D)
+        out = torch.zeros(T, D if part == "gate_up" else H, dtype=BF16, device="cuda")
+        ws = torch.empty(abi.moe_operator_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+        abi.moe_grouped_linear_int8(cfg, part, q[:T], s[:T], w_q, w_s, off, out, ws)
+        assert abi.moe_device_status(ws) == 0 and not out[rows:].any()
+        outs.append(out[:rows])
+    assert outs[0].any() and all(torch.equal(o, outs[0]) for o in outs)
+
+
+@pytest.mark.parametrize("H,D", [(2056, 64), (72, 2504)], ids=["shared_k", "whole_k"])
+def test_grouped_linear_int8_offsets_written_just_before(H, D):
+    """Offsets that the kernel right before writes: the product may have begun when they
+    were still those of the call before, and goes by the new ones."""
+    T, E, k = 40, 6, 2
+    cfg = abi.config(T, H, E, k, D)
+    R_ = T * k
+    idx = [R.routing(T, E, k, seed=i, drop=0.3 * i, one_expert=4 if i == 2 else None)[0].cuda() for i in range(3)]
+    g = torch.Generator().manual_seed(9)
+    q = torch.randint(-127, 128, (R_, abi.int8_pitch(H)), generator=g, dtype=torch.int8).cuda()
+    w_q = torch.randint(-127, 128, (E, 2 * D, abi.int8_pitch(H)), generator=g, dtype=torch.int8).cuda()
+    s, w_s = (torch.rand(R_, generator=g) * 0.02).cuda(), (torch.rand(E, 2 * D, generator=g) * 0.002).cuda()
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    perm, inv = torch.zeros(R_, dtype=torch.int32, device="cuda"), torch.zeros(R_, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(abi.moe_workspace_size(cfg), abi.moe_operator_workspace_size(cfg)), dtype=torch.uint8, device="cuda")
+    ows = torch.empty(abi.moe_operator_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    want = []
+    for i in range(3):
+        out = torch.zeros(R_, D, dtype=BF16, device="cuda")
+        abi.moe_create_indices(cfg, idx[i], off, perm, inv, ws)
+        torch.cuda.synchronize()
+        abi.moe_grouped_linear_int8(cfg, "gate_up", q, s, w_q, w_s, off, out, ows)
+        torch.cuda.synchronize()
+        want.append(out)
+    assert not torch.equal(want[0], want[1]) and not torch.equal(want[0], want[2])
+    outs = [torch.zeros(R_, D, dtype=BF16, device="cuda") for _ in range(60)]
+    for i, out in enumerate(outs):
+        abi.moe_create_indices(cfg, idx[i % 3], off, perm, inv, ws)
+        abi.moe_grouped_linear_int8(cfg, "gate_up", q, s, w_q, w_s, off, out, ows)
+    assert all(torch.equal(out, want[i % 3]) for i, out in enumerate(outs))
+
+
 def test_grouped_linear_int8_same_bits_in_every_tile_shape():
     """A row's product does not depend on how many rows its expert has, nor on the
     kernel that takes them."""
