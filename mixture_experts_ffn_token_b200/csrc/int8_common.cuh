@@ -139,4 +139,44 @@ __device__ __forceinline__ void build_pieces(const int* s_off, int* s_mt, int* b
   if (__any_sync(0xffffffffu, bad) && lane == 0) *bad_flag = 1;
 }
 
+// Reads and checks the offsets and builds s_mt; returns the number of pieces, 0
+// for offsets that are no CSR (recorded in *status).  While the kernels before
+// (as a rule the rows' quantiser) still run, `prefetch` is called by warp 0 to
+// fetch the first tile's weights to L2, where their copies then find them: a
+// hint, which cannot make a value stale.  The offsets that it goes by may still
+// be changing, so it gets any CSR, and they are read again afterwards.  On return
+// the kernels before are complete and visible.
+template <typename Prefetch>
+__device__ __forceinline__ int csr_pieces(const Int8Params& g, int* s_off, int* s_mt, int* bad_flag, int piece,
+                                          Prefetch prefetch) {
+  const int lane = threadIdx.x & 31;
+  auto read = [&]() {
+    for (int i = threadIdx.x; i <= g.E; i += blockDim.x) s_off[i] = __ldcg(g.offsets + i);
+  };
+  if (threadIdx.x == 0) *bad_flag = 0;
+  read();
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    build_pieces(s_off, s_mt, bad_flag, g.E, g.R, piece, lane);
+    __syncwarp();
+    if (*bad_flag == 0) prefetch();
+  }
+  griddep_wait();
+  // the status word of this call starts at zero: only this CTA records a bad
+  // CSR, and a timed-out wait of another comes seconds later
+  if (blockIdx.x == 0 && threadIdx.x == 0) *g.status = 0;
+  bool same = true;
+  for (int i = threadIdx.x; i <= g.E; i += blockDim.x) same = same && s_off[i] == __ldcg(g.offsets + i);
+  if (!__syncthreads_and(same)) {
+    if (threadIdx.x == 0) *bad_flag = 0;
+    read();
+    __syncthreads();
+    if (threadIdx.x < 32) build_pieces(s_off, s_mt, bad_flag, g.E, g.R, piece, lane);
+    __syncthreads();
+  }
+  const bool bad = *bad_flag != 0;
+  if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(g.status, MOE_DEVICE_ERR_CSR);
+  return bad ? 0 : s_mt[g.E];
+}
+
 }  // namespace moe

@@ -150,7 +150,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
-    *bad_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&mapB);
     tma_prefetch_map(&mapA16);
@@ -159,44 +158,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
-  // While the kernels before (as a rule the rows' quantiser) still run, the first
-  // tile's weights are fetched to L2, where their copies then find them: a hint,
-  // which cannot make a value stale.  The offsets that it goes by may still be
-  // changing, so it takes any CSR, and they are read again afterwards.
-  __syncthreads();
-  for (int i = threadIdx.x; i <= p.g.E; i += NUM_THREADS) s_off[i] = __ldcg(p.g.offsets + i);
-  __syncthreads();
-  if (warp == 0) {
-    build_pieces(s_off, s_mt, bad_flag, p.g.E, p.g.R, BR, lane);
-    __syncwarp();
-    const int t = first;
-    if (*bad_flag == 0 && t < s_mt[p.g.E] * p.g.n_tiles) {
-      const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
-      for (int kb = kb0 + lane; kb < min(kb1, kb0 + p.ahead); kb += 32) {
-        if constexpr (MODE == MODE_CONCAT) tma_prefetch_5d(&mapB, kb * BK, 0, 0, tc.n * (p.wc / 16), tc.e);
-        else tma_prefetch_3d(&mapB, kb * BK, tc.n * p.wc, tc.e);
-      }
+  const int pieces = csr_pieces(p.g, s_off, s_mt, bad_flag, BR, [&]() {
+    if (first >= s_mt[p.g.E] * p.g.n_tiles) return;
+    const TileCoord tc = decode_tile(first, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+    for (int kb = kb0 + lane; kb < min(kb1, kb0 + p.ahead); kb += 32) {
+      if constexpr (MODE == MODE_CONCAT) tma_prefetch_5d(&mapB, kb * BK, 0, 0, tc.n * (p.wc / 16), tc.e);
+      else tma_prefetch_3d(&mapB, kb * BK, tc.n * p.wc, tc.e);
     }
-  }
-  griddep_wait();  // the offsets and operands of the kernels before are complete and visible
-  // the status word of this call starts at zero: only this CTA records a bad
-  // CSR, and a timed-out wait of another comes seconds later
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.g.status = 0;
-  bool same = true;
-  for (int i = threadIdx.x; i <= p.g.E; i += NUM_THREADS) same = same && s_off[i] == __ldcg(p.g.offsets + i);
-  if (!__syncthreads_and(same)) {
-    for (int i = threadIdx.x; i <= p.g.E; i += NUM_THREADS) s_off[i] = __ldcg(p.g.offsets + i);
-    if (threadIdx.x == 0) *bad_flag = 0;
-    __syncthreads();
-    if (warp == 0) build_pieces(s_off, s_mt, bad_flag, p.g.E, p.g.R, BR, lane);
-  }
+  });
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  const bool bad = *bad_flag != 0;
-  if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.g.status, MOE_DEVICE_ERR_CSR);
-  const int total = bad ? 0 : s_mt[p.g.E] * p.g.n_tiles;
+  const int total = pieces * p.g.n_tiles;
   const int w_bytes = p.wc * BK, stage_bytes = w_bytes + p.cap * BK;
 
   // Both single-thread roles run as whole warps of which one lane issues: then
@@ -464,12 +438,16 @@ cudaError_t launch_mode(const Int8GemmArgs& a, int wc, cudaStream_t stream) {
   const cuuint64_t pitch = static_cast<cuuint64_t>(int8_pitch(K));
   const cuuint64_t N = down ? a.H : 2 * static_cast<cuuint64_t>(a.D), E = a.E;
   constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  // a tile has at most R rows: one token's few rows leave room for more stages,
+  // and need fewer maps (0.4 us of the host's time each)
+  const int cap = a.R <= 16 ? 16 : a.R <= 32 ? 32 : a.R <= 64 ? 64 : BR;
   CUtensorMap mapA[4], mapB;
   for (int i = 0; i < 4; ++i) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(a.R)};
     const cuuint64_t strides[1] = {pitch};
     const cuuint32_t box[2] = {BK, 16u << i};
-    if (!encode_tiled_map(&mapA[i], kU8, a.A, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    if ((16 << i) > cap) mapA[i] = mapA[i - 1];  // (no tile asks for it)
+    else if (!encode_tiled_map(&mapA[i], kU8, a.A, 2, dims, strides, box)) return cudaErrorInvalidValue;
   }
   if (MODE == MODE_CONCAT) {
     const cuuint64_t D = a.D;
@@ -490,8 +468,7 @@ cudaError_t launch_mode(const Int8GemmArgs& a, int wc, cudaStream_t stream) {
   p.g.num_kb = (K + BK - 1) / BK;
   p.wc = wc;
   p.blocks = wc / MMA_COLS;
-  // a tile has at most R rows: one token's few rows leave room for more stages
-  p.cap = a.R <= 16 ? 16 : a.R <= 32 ? 32 : a.R <= 64 ? 64 : BR;
+  p.cap = cap;
   p.stages = std::min(MAX_STAGES, RING_BYTES / ((wc + p.cap) * BK));
   p.ahead = std::min(p.g.num_kb, AHEAD_BYTES / (wc * BK));
   const int64_t max_tiles = (static_cast<int64_t>(a.R) / BR + std::min(a.E, a.R)) * p.g.n_tiles;

@@ -240,7 +240,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
-    *bad_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&mapA);
     tma_prefetch_map(&mapB);
@@ -249,20 +248,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
-  griddep_wait();  // the offsets and operands of the kernels before are complete and visible
-  // the status word of this call starts at zero: only this CTA records a bad
-  // CSR, and a timed-out wait of another comes seconds later
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-  for (int i = threadIdx.x; i <= p.E; i += NUM_THREADS) s_off[i] = p.offsets[i];
-  __syncthreads();
-  if (warp == 0) build_pieces(s_off, s_mt, bad_flag, p.E, p.R, BM, lane);
+  const int pieces = csr_pieces(p, s_off, s_mt, bad_flag, BM, [&]() {
+    const int t = blockIdx.x;
+    if (t >= s_mt[p.E] * p.n_tiles) return;
+    const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
+    if (lane < min(p.num_kb, STAGES)) {
+      if constexpr (MODE == MODE_CONCAT) tma_prefetch_4d(&mapB, lane * BK, tc.n * (BN / 2), 0, tc.e);
+      else tma_prefetch_3d(&mapB, lane * BK, tc.n * BN, tc.e);
+    }
+  });
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  const bool bad = *bad_flag != 0;
-  if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, MOE_DEVICE_ERR_CSR);
-  const int total = bad ? 0 : s_mt[p.E] * p.n_tiles;
+  const int total = pieces * p.n_tiles;
 
   if (warp == 0) {
     if (lane == 0) {
