@@ -139,6 +139,30 @@ __device__ __forceinline__ void build_pieces(const int* s_off, int* s_mt, int* b
   if (__any_sync(0xffffffffu, bad) && lane == 0) *bad_flag = 1;
 }
 
+// Tile t as decode_tile gives it, by a whole warp (all lanes, the same t): the
+// expert is looked for from `from` on (at most t's), 32 experts at a time, which
+// takes one step where decode_tile's halving takes log2(E) dependent ones.
+__device__ __forceinline__ TileCoord warp_tile(int t, int from, int n_tiles, int E, const int* s_mt, const int* s_off,
+                                               int piece) {
+  const int lane = threadIdx.x & 31;
+  int e = from;
+  for (;;) {
+    const int i = e + 1 + lane;
+    const int ahead = __popc(__ballot_sync(0xffffffffu, i < E && s_mt[i < E ? i : E] * n_tiles <= t));
+    e += ahead;
+    if (ahead < 32) break;
+  }
+  TileCoord c;
+  c.e = e;
+  const int local = t - s_mt[e] * n_tiles, mt = s_mt[e + 1] - s_mt[e];
+  c.n = mt == 1 ? local : local / mt;
+  const int m = local - c.n * mt;
+  c.row0 = s_off[e] + m * piece;
+  c.rows = min(piece, s_off[e + 1] - c.row0);
+  c.piece = s_mt[e] + m;
+  return c;
+}
+
 // Reads and checks the offsets and builds s_mt; returns the number of pieces, 0
 // for offsets that are no CSR (recorded in *status).  While the kernels before
 // (as a rule the rows' quantiser) still run, `prefetch` is called by warp 0 to

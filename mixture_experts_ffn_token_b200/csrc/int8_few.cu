@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   const int pieces = csr_pieces(p.g, s_off, s_mt, bad_flag, BR, [&]() {
     if (first >= s_mt[p.g.E] * p.g.n_tiles) return;
-    const TileCoord tc = decode_tile(first, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+    const TileCoord tc = warp_tile(first, 0, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
     for (int kb = kb0 + lane; kb < min(kb1, kb0 + p.ahead); kb += 32) {
       if constexpr (MODE == MODE_CONCAT) tma_prefetch_5d(&mapB, kb * BK, 0, 0, tc.n * (p.wc / 16), tc.e);
       else tma_prefetch_3d(&mapB, kb * BK, tc.n * p.wc, tc.e);
@@ -187,12 +187,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // the loops' values are uniform.
   if (warp == 0) {
     // ---------------------------------------------------- TMA producer
-    int it = 0, s = 0;
+    int it = 0, s = 0, e = 0;
     uint32_t ph = 0;
     bool ok = true;
     const bool leader = elect_one();
     for (int t = first; ok && t < total; t += step) {
-      const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+      const TileCoord tc = warp_tile(t, e, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+      e = tc.e;
       // the smallest box that holds the rows
       const int rows = tc.rows <= 16 ? 16 : tc.rows <= 32 ? 32 : tc.rows <= 64 ? 64 : 128;
       const CUtensorMap* ma = rows == 16 ? &mapA16 : rows == 32 ? &mapA32 : rows == 64 ? &mapA64 : &mapA128;
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer
-    int s = 0, ti = 0;
+    int s = 0, ti = 0, e = 0;
     uint32_t ph = 0;
     bool ok = true;
     const bool leader = elect_one();
@@ -252,7 +253,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       tc_fence_after_sync();
       const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 2 * BR);
-      const TileCoord tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+      const TileCoord tc = warp_tile(t, e, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+      e = tc.e;
       const uint32_t idesc = idesc_s8_s32(MMA_COLS, (tc.rows + 15) & ~15);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, ph, abort_flag, kTimeoutNs))) {
@@ -301,9 +303,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float ws, bias;        // and its column of W's
       float rs[BR / 32];     // scales of rows lane, lane + 32, ...
     };
-    auto fetch = [&](int t) {
+    auto fetch = [&](int t, int from) {
       Ahead f;
-      f.tc = decode_tile(t, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
+      f.tc = warp_tile(t, from, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
       int wcol;
       if constexpr (MODE == MODE_CONCAT) {
         f.col = f.tc.n * (p.wc / 2) + (wrow >> 4) * 8 + (wrow & 7);
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       return f;
     };
     Ahead next = {};
-    if (first < total) next = fetch(first);
+    if (first < total) next = fetch(first, 0);
     if constexpr (SPLIT) {
       const TileCoord tc = next.tc;
 #pragma unroll
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
       for (int i = 0; i < BR / 32; ++i) scales[lane + 32 * i] = next.rs[i];
       __syncwarp();
-      if (t + step < total) next = fetch(t + step);
+      if (t + step < total) next = fetch(t + step, tc.e);
       const bool got = mbar_wait(tfull0 + 8 * acc, static_cast<uint32_t>(ti >> 1) & 1u, abort_flag, kTimeoutNs);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after_sync();

@@ -94,10 +94,10 @@ struct Ahead {
   uint2 b;
 };
 template <int MODE>
-__device__ __forceinline__ Ahead fetch(const Int8Params& p, int t, const int* s_mt, const int* s_off, int quad, int part,
+__device__ __forceinline__ Ahead fetch(const Int8Params& p, int t, int from, const int* s_mt, const int* s_off, int quad, int part,
                                        int lane) {
   Ahead f;
-  f.tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
+  f.tc = warp_tile(t, from, p.n_tiles, p.E, s_mt, s_off, BM);
   f.w = warp_part<MODE>(f.tc.n, quad, part, f.tc.rows <= HALF_ROWS);
   f.rs = lane < f.w.lanes && f.w.row0 + lane < f.tc.rows ? __ldg(p.a_scales + f.tc.row0 + f.w.row0 + lane) : 0.f;
   int c = -1;  // the group's first weight column, or -1 past the end
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // (a whole warp of which one lane issues: then the loop's values are uniform,
     // and an MMA costs the thread no 40 cycles: E 8, 4096 x 28672, 8192 rows 827 ->
     // 800 us; the copying warp likewise makes a short K slower, 75.6 -> 77.6)
-    int s = 0, ti = 0;
+    int s = 0, ti = 0, e = 0;
     uint32_t ph = 0;
     bool ok = true;
     const bool leader = elect_one();
@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       tc_fence_after_sync();
       const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-      const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
+      const TileCoord tc = warp_tile(t, e, p.n_tiles, p.E, s_mt, s_off, BM);
+      e = tc.e;
       const uint32_t idesc = tc.rows <= HALF_ROWS ? idesc_s8_s32(HALF_ROWS, BN) : idesc_s8_s32(BM, BN);
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, ph, abort_flag, kTimeoutNs))) {
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int part = (warp - 2) >> 2;  // which half of the tile's columns
     uint8_t* stage = s_stage + (warp - 2) * kWarpStage;
     Ahead next = {};
-    if (static_cast<int>(blockIdx.x) < total) next = fetch<MODE>(p, blockIdx.x, s_mt, s_off, quad, part, lane);
+    if (static_cast<int>(blockIdx.x) < total) next = fetch<MODE>(p, blockIdx.x, 0, s_mt, s_off, quad, part, lane);
     int ti = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
       const int acc = ti & 1;
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       *reinterpret_cast<uint2*>(stage + kBiasAt + 8 * lane) = next.b;
       __syncwarp();
       if (t + static_cast<int>(gridDim.x) < total)
-        next = fetch<MODE>(p, t + gridDim.x, s_mt, s_off, quad, part, lane);
+        next = fetch<MODE>(p, t + gridDim.x, tc.e, s_mt, s_off, quad, part, lane);
       const bool got = mbar_wait(tfull0 + 8 * acc, static_cast<uint32_t>(ti >> 1) & 1u, abort_flag, kTimeoutNs);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after_sync();
