@@ -837,6 +837,58 @@ def test_two_calls_at_once():
         assert torch.equal(j["h"], w) and abi.moe_device_status(j["ws"]) == 0
 
 
+def test_int8_shared_k_captured_and_at_once():
+    """A K shared by blocks, captured: two graphs (a workspace each) replayed on two
+    streams at the same time, on inputs that change between the replays."""
+    T, H, D, E, k = 6, 4104, 136, 4, 2
+    cfg = abi.config(T, H, E, k, D)
+    g = torch.Generator().manual_seed(8)
+    w_q = torch.randint(-127, 128, (E, 2 * D, abi.int8_pitch(H)), generator=g, dtype=torch.int8).cuda()
+    w_s = (torch.rand(E, 2 * D, generator=g) * 0.002).cuda()
+    xs = [randn(40 + i, T, H, dtype=BF16).cuda() for i in range(4)]
+    routes = [[t.cuda() for t in R.routing(T, E, k, seed=50 + i, drop=0.2)[1:]] for i in range(4)]
+
+    def job():
+        return dict(x=xs[0].clone(), off=routes[0][0].clone(), inv=routes[0][1].clone(),
+                    q=torch.zeros(T * k, abi.int8_pitch(H), dtype=torch.int8, device="cuda"), s=torch.zeros(T * k, device="cuda"),
+                    h=torch.zeros(T * k, D, dtype=BF16, device="cuda"),
+                    ws=torch.empty(abi.moe_operator_workspace_size(cfg), dtype=torch.uint8, device="cuda"))
+
+    def run(j):
+        j["h"].zero_()
+        abi.moe_dispatch_int8(cfg, j["x"], j["inv"], j["q"], j["s"])
+        abi.moe_grouped_linear_int8(cfg, "gate_up", j["q"], j["s"], w_q, w_s, j["off"], j["h"], j["ws"])
+
+    def load(j, i):
+        j["x"].copy_(xs[i]), j["off"].copy_(routes[i][0]), j["inv"].copy_(routes[i][1])
+
+    plain, want = job(), []
+    for i in range(4):
+        load(plain, i)
+        run(plain)
+        torch.cuda.synchronize()
+        want.append(plain["h"].clone())
+    assert all(w.any() for w in want) and not torch.equal(want[0], want[1])
+    jobs, graphs, streams = [job(), job()], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for j, st in zip(jobs, streams):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=st):
+            run(j)
+        graphs.append(gr)
+    torch.cuda.synchronize()
+    for i in range(12):
+        got = []
+        for n, (j, st) in enumerate(zip(jobs, streams)):
+            with torch.cuda.stream(st):
+                load(j, (i + n) % 4)
+                graphs[n].replay()
+                got.append(j["h"].clone())
+        torch.cuda.synchronize()
+        for n, h in enumerate(got):
+            assert torch.equal(h, want[(i + n) % 4]) and abi.moe_device_status(jobs[n]["ws"]) == 0
+
+
 def test_backward_captured_and_on_a_given_stream():
     T, H, E, k = 300, 520, 16, 3
     cfg = abi.config(T, H, E, k, 8, logits_dtype=F32)
