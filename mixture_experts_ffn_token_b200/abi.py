@@ -361,6 +361,34 @@ def moe_device_status(workspace, stream=None) -> int:
 # gradient, and the experts' products in 8-bit integers.  These check their
 # tensors (type, size, dense layout, the current device) before the call: a
 # ValueError means that nothing was enqueued.
+# The checks and the call are one step in _binding.so; where it finds something
+# that is not as it should be, they are made again here, for the error's text.
+
+_binding = None
+
+
+def _load_binding():
+    """Load _binding.so (raises OSError when it has not been built)."""
+    global _binding
+    lib = load_library()
+    try:
+        from . import _binding as b
+    except ImportError as e:
+        raise OSError(f"_binding.so cannot be loaded ({e}): build it with "
+                      "`python -m mixture_experts_ffn_token_b200.build`") from e
+    b.use(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+        "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward", "moe_route_backward",
+        "moe_dispatch_int8", "moe_quantize_rows", "moe_grouped_linear_int8")))
+    _binding = b
+    return b
+
+
+def _done(status: int, where: str) -> bool:
+    """Whether the call is made (False: an argument is not as it should be)."""
+    if status > 0:
+        raise MoEError(status, where)
+    return status == 0
+
 
 def _take(device, name, t, dtype, numel, required=True):
     """The data pointer of a dense tensor of `numel` elements on the current device."""
@@ -422,6 +450,9 @@ def moe_operator_workspace_size(cfg: MoEConfig) -> int:
 def moe_dispatch(cfg, x, inverse, rows, expert_weights=None, stream=None):
     """rows[inverse[t*k+j]] = expert_weights[t, j] * x[t]: tokens [T, H] (bf16
     or fp32) to rows sorted by expert [T*k, H]."""
+    st = (_binding or _load_binding()).dispatch(cfg, x, inverse, rows, expert_weights, stream)
+    if _done(st, "moe_dispatch"):
+        return
     dt, dev = _rows_dtype("x", x), _device()
     T, H = cfg.num_tokens, cfg.hidden_dim
     R = T * cfg.top_k
@@ -434,6 +465,10 @@ def moe_dispatch(cfg, x, inverse, rows, expert_weights=None, stream=None):
 def moe_dispatch_backward(cfg, d_rows, inverse, d_x, x=None, expert_weights=None, d_expert_weights=None, stream=None):
     """d_x[t] = sum_j expert_weights[t, j] * d_rows[inverse[t*k+j]] and, given x,
     d_expert_weights[t, j] = <x[t], d_rows[inverse[t*k+j]]>."""
+    st = (_binding or _load_binding()).dispatch_backward(cfg, d_rows, inverse, d_x, x, expert_weights,
+        d_expert_weights, stream)
+    if _done(st, "moe_dispatch_backward"):
+        return
     dt, dev = _rows_dtype("d_rows", d_rows), _device()
     T, H = cfg.num_tokens, cfg.hidden_dim
     R = T * cfg.top_k
@@ -449,6 +484,9 @@ def moe_dispatch_backward(cfg, d_rows, inverse, d_x, x=None, expert_weights=None
 
 def moe_combine(cfg, rows, inverse, out, expert_weights=None, stream=None):
     """out[t] = sum_j expert_weights[t, j] * rows[inverse[t*k+j]]."""
+    st = (_binding or _load_binding()).combine(cfg, rows, inverse, out, expert_weights, stream)
+    if _done(st, "moe_combine"):
+        return
     dt, dev = _rows_dtype("rows", rows), _device()
     T, H = cfg.num_tokens, cfg.hidden_dim
     R = T * cfg.top_k
@@ -463,6 +501,10 @@ def moe_combine_backward(cfg, d_out, inverse, d_rows, rows=None, expert_weights=
                          stream=None):
     """d_rows[inverse[t*k+j]] = expert_weights[t, j] * d_out[t] and, given rows,
     d_expert_weights[t, j] = <d_out[t], rows[inverse[t*k+j]]>."""
+    st = (_binding or _load_binding()).combine_backward(cfg, d_out, inverse, d_rows, rows, expert_weights,
+        d_expert_weights, stream)
+    if _done(st, "moe_combine_backward"):
+        return
     dt, dev = _rows_dtype("d_out", d_out), _device()
     T, H = cfg.num_tokens, cfg.hidden_dim
     R = T * cfg.top_k
@@ -481,6 +523,10 @@ def moe_route_backward(cfg, logits, expert_indices, d_expert_weights, d_logits, 
     """d_logits [T, logits_row_stride] (and d_global_scale [1], which needs a
     workspace of moe_operator_workspace_size) from the gradients of the
     weights that moe_route returned for expert_indices."""
+    st = (_binding or _load_binding()).route_backward(cfg, logits, expert_indices, d_expert_weights, d_logits,
+        d_sink_weights, global_scale, d_global_scale, workspace, stream)
+    if _done(st, "moe_route_backward"):
+        return
     dev = _device()
     T, k, S, n = cfg.num_tokens, cfg.top_k, cfg.num_sink, cfg.num_tokens * cfg.logits_row_stride
     dt = torch.bfloat16 if cfg.logits_dtype == DTYPES[torch.bfloat16] else torch.float32
@@ -500,6 +546,9 @@ def moe_route_backward(cfg, logits, expert_indices, d_expert_weights, d_logits, 
 
 def moe_dispatch_int8(cfg, x, inverse, rows_q, row_scales, stream=None):
     """moe_dispatch of bf16 tokens to 8-bit rows [T*k, int8_pitch(H)] and their scales [T*k]."""
+    st = (_binding or _load_binding()).dispatch_int8(cfg, x, inverse, rows_q, row_scales, stream)
+    if _done(st, "moe_dispatch_int8"):
+        return
     dev = _device()
     T, H = cfg.num_tokens, cfg.hidden_dim
     R = T * cfg.top_k
@@ -512,6 +561,9 @@ def moe_dispatch_int8(cfg, x, inverse, rows_q, row_scales, stream=None):
 def moe_quantize_rows(cfg, h, expert_offsets, rows_q, row_scales, stream=None):
     """Activations h [T*k, D] bf16 to 8-bit rows [T*k, int8_pitch(D)] and their
     scales, up to row expert_offsets[E] (None: all)."""
+    st = (_binding or _load_binding()).quantize_rows(cfg, h, expert_offsets, rows_q, row_scales, stream)
+    if _done(st, "moe_quantize_rows"):
+        return
     dev = _device()
     D, R = cfg.moe_dim, cfg.num_tokens * cfg.top_k
     _check(load_library().moe_quantize_rows(
@@ -544,6 +596,10 @@ def moe_grouped_linear_int8(cfg, contraction, rows_q, row_scales, w_q, w_scales,
                             bias=None, stream=None):
     """One contraction over rows sorted by expert, in 8-bit integers: "gate_up"
     with the activation to out [T*k, D], "down" to out [T*k, H] (bf16)."""
+    st = (_binding or _load_binding()).grouped_linear_int8(cfg, CONTRACTIONS.get(contraction), rows_q, row_scales, w_q,
+        w_scales, expert_offsets, out, workspace, bias, stream)
+    if _done(st, "moe_grouped_linear_int8"):
+        return
     (which, K, N), dev, E = _contraction(cfg, contraction), _device(), cfg.num_experts
     R = cfg.num_tokens * cfg.top_k
     _check(load_library().moe_grouped_linear_int8(

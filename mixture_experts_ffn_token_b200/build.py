@@ -1,21 +1,26 @@
-"""Build the sm_100a CUDA library libmoe_b200.so in-tree (next to this file).
+"""Build the sm_100a CUDA library libmoe_b200.so and its Python binding in-tree
+(next to this file).
 
     python -m mixture_experts_ffn_token_b200.build [--verbose-ptxas]
 
 nvcc compiles every csrc/*.cu for sm_100a only and links one shared library
 exporting the C ABI of include/moe.h (the CUDA runtime is linked statically).
+g++ compiles csrc/binding.cpp, which reads torch's tensors, to _binding.so.
 """
 import argparse
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_b200.so")
+BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CUDA_HOME = os.path.dirname(os.path.dirname(NVCC))
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2"]
 
@@ -25,14 +30,14 @@ def sources():
 
 
 def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
+    return sources() + [os.path.join(CSRC, "binding.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + [
         os.path.join(os.path.dirname(HERE), "include", "moe.h"), __file__]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -51,7 +56,21 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     tmp = LIB + ".tmp"
     subprocess.run([NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp], check=True)
     os.replace(tmp, LIB)
+    build_binding()
     return LIB
+
+
+def build_binding():
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(CUDA_HOME, "include")]
+    tmp = BINDING + ".tmp"
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                    os.path.join(CSRC, "binding.cpp"), "-o", tmp, *(f"-I{d}" for d in include),
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-L" + os.path.join(root, "lib"),
+                    "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

@@ -927,7 +927,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 // same shapes, call after call).
 struct MapKey {
   const void* base;
-  CUtensorMapDataType type;
   int rank;
   cuuint64_t dims[5];
   cuuint64_t strides[4];
@@ -935,7 +934,7 @@ struct MapKey {
 };
 
 bool same_key(const MapKey& a, const MapKey& b) {
-  if (a.base != b.base || a.type != b.type || a.rank != b.rank) return false;
+  if (a.base != b.base || a.rank != b.rank) return false;
   for (int i = 0; i < a.rank; ++i)
     if (a.dims[i] != b.dims[i] || a.box[i] != b.box[i]) return false;
   for (int i = 0; i + 1 < a.rank; ++i)
@@ -956,9 +955,20 @@ thread_local MapCache t_maps;
 
 bool encode_tiled_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
                       const cuuint64_t* strides_bytes, const cuuint32_t* box) {
+  auto enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
+  return enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides_bytes, box, elem_strides,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                     const cuuint64_t* strides_bytes, const cuuint32_t* box) {
   MapKey key = {};
   key.base = base;
-  key.type = type;
   key.rank = rank;
   for (int i = 0; i < rank; ++i) {
     key.dims[i] = dims[i];
@@ -972,14 +982,7 @@ bool encode_tiled_map(CUtensorMap* map, CUtensorMapDataType type, const void* ba
       return true;
     }
   }
-  auto enc = encoder();
-  if (enc == nullptr) return false;
-  const cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
-  const CUresult r = enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base),
-                         dims, strides_bytes, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return false;
+  if (!encode_tiled_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides_bytes, box)) return false;
   int slot;
   if (c.used < kMapCacheSize) {
     slot = c.used++;
@@ -990,13 +993,6 @@ bool encode_tiled_map(CUtensorMap* map, CUtensorMapDataType type, const void* ba
   c.key[slot] = key;
   c.map[slot] = *map;
   return true;
-}
-
-namespace {
-
-bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
-                     const cuuint64_t* strides_bytes, const cuuint32_t* box) {
-  return encode_tiled_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides_bytes, box);
 }
 
 template <int PAIR>

@@ -452,7 +452,7 @@ cudaError_t launch_mode(const Int8GemmArgs& a, int wc, cudaStream_t stream) {
   const cuuint64_t N = down ? a.H : 2 * static_cast<cuuint64_t>(a.D), E = a.E;
   constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   // a tile has at most R rows: one token's few rows leave room for more stages,
-  // and need fewer maps (0.4 us of the host's time each)
+  // and need fewer maps
   const int cap = a.R <= 16 ? 16 : a.R <= 32 ? 32 : a.R <= 64 ? 64 : BR;
   CUtensorMap mapA[4], mapB;
   for (int i = 0; i < 4; ++i) {

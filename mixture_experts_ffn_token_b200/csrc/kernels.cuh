@@ -186,8 +186,7 @@ int mega_ffn_counters(int R, int E);
 cudaError_t launch_mega_ffn(const GroupedGemmArgs& up, const GroupedGemmArgs& down, int* arrivals,
                             cudaStream_t stream);
 
-// Encodes (or takes from a small per-thread cache) a 128-byte-swizzled tensor
-// map of `rank` dimensions; strides in bytes, from the second dimension on.
+// Encodes a 128-byte-swizzled tensor map of `rank` dimensions; strides in bytes, from the second dimension on.
 bool encode_tiled_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
                       const cuuint64_t* strides_bytes, const cuuint32_t* box);
 

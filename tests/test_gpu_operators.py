@@ -920,3 +920,72 @@ def test_backward_captured_and_on_a_given_stream():
             graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, (d_x, d_rows, d_w, d_l))), run
+
+
+# ---------------------------------------------------------------- refusals
+def _calls():
+    """Every operator with arguments that are as they should be, by name."""
+    T, H, D, E, k, S = 5, 64, 48, 4, 2, 2
+    R_ = T * k
+    cfg = abi.config(T, H, E, k, D, router="sigmoid_sink", num_sink=S)
+    z = lambda *shape, dt=F32: torch.zeros(shape, dtype=dt, device="cuda")  # noqa: E731
+    i8, u8, i32 = torch.int8, torch.uint8, torch.int32
+    ws = z(abi.moe_operator_workspace_size(cfg), dt=u8)
+    inv = torch.arange(R_, dtype=i32, device="cuda")
+    off = torch.tensor([0, 4, 4, 6, 10], dtype=i32, device="cuda")
+    x, rows, w, dw = z(T, H, dt=BF16), z(R_, H, dt=BF16), z(T, k), z(T, k)
+    q = dict(gate_up=z(R_, abi.int8_pitch(H), dt=i8), down=z(R_, abi.int8_pitch(D), dt=i8))
+    lin = lambda part, K, N, n: dict(  # noqa: E731
+        cfg=cfg, contraction=part, rows_q=q[part], row_scales=z(R_), w_q=z(E, N, abi.int8_pitch(K), dt=i8), w_scales=z(E, N),
+        expert_offsets=off, out=z(R_, n, dt=BF16), workspace=ws)
+    return {
+        "moe_dispatch": [dict(cfg=cfg, x=x, inverse=inv, rows=rows, expert_weights=w)],
+        "moe_dispatch_backward": [dict(cfg=cfg, d_rows=rows, inverse=inv, d_x=z(T, H, dt=BF16), x=x, expert_weights=w,
+                                       d_expert_weights=dw)],
+        "moe_combine": [dict(cfg=cfg, rows=rows, inverse=inv, out=x, expert_weights=w)],
+        "moe_combine_backward": [dict(cfg=cfg, d_out=x, inverse=inv, d_rows=z(R_, H, dt=BF16), rows=rows, expert_weights=w,
+                                      d_expert_weights=dw)],
+        "moe_route_backward": [dict(cfg=cfg, logits=z(T, E + S), expert_indices=z(T, k, dt=i32), d_expert_weights=w,
+                                    d_logits=z(T, E + S), d_sink_weights=z(T, S), global_scale=z(1), d_global_scale=z(1),
+                                    workspace=ws)],
+        "moe_dispatch_int8": [dict(cfg=cfg, x=x, inverse=inv, rows_q=q["gate_up"], row_scales=z(R_))],
+        "moe_quantize_rows": [dict(cfg=cfg, h=z(R_, D, dt=BF16), expert_offsets=off, rows_q=q["down"], row_scales=z(R_))],
+        "moe_grouped_linear_int8": [lin("gate_up", H, 2 * D, D), lin("down", D, H, H)],
+    }
+
+
+@pytest.mark.parametrize("name", ["moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+                                  "moe_route_backward", "moe_dispatch_int8", "moe_quantize_rows", "moe_grouped_linear_int8"])
+def test_each_tensor_that_is_not_as_it_should_be_is_refused(name):
+    call = getattr(abi, name)
+    for good in _calls()[name]:
+        call(**good)
+        call(**good, stream=torch.cuda.Stream())
+        torch.cuda.synchronize()
+        outputs = {n: t.clone() for n, t in good.items() if isinstance(t, torch.Tensor)}
+        for arg, t in good.items():
+            if not isinstance(t, torch.Tensor):
+                continue
+            bad = [t.cpu(), t.double(), t.to(torch.int16)]
+            if arg != "workspace":  # (any size, which the library checks)
+                bad.append(torch.cat([t.reshape(-1), t.reshape(-1)[:1]]))
+                if t.numel() > 1:
+                    bad.append(torch.stack([t, t], -1)[..., 0])
+            else:
+                bad.append(torch.stack([t, t], -1)[..., 0])
+            for b in bad:
+                with pytest.raises(ValueError, match=arg if t.dtype is not BF16 else "bfloat16|float32|" + arg):
+                    call(**{**good, arg: b})
+        with pytest.raises((ValueError, abi.MoEError)):
+            call(**{**good, next(n for n, t in good.items() if isinstance(t, torch.Tensor)): None})
+        with pytest.raises(AttributeError):
+            call(**good, stream=7)
+        torch.cuda.synchronize()
+        assert all(torch.equal(good[n], t) for n, t in outputs.items())
+    if name == "moe_grouped_linear_int8":
+        with pytest.raises(ValueError, match="contraction"):
+            call(**{**good, "contraction": "up"})
+        with pytest.raises(abi.MoEError):
+            call(**{**good, "workspace": good["workspace"][:16]})
+        with pytest.raises(abi.MoEError):
+            call(**{**good, "bias": torch.zeros(4, 64, dtype=BF16, device="cuda")})  # (cfg.has_bias is 0)
