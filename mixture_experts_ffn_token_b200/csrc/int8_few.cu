@@ -7,15 +7,17 @@
 //
 // Tiles are `wc` weight columns (256, or 128 where that leaves SMs without a
 // tile) by up to 128 rows.  Roles are those of int8_gemm.cu; a stage holds wc x
-// 128 B of W and 128 x 128 B of rows, of which the smallest box (16 to 128 rows)
-// that holds the tile's is copied.
+// 128 B of W and the rows that a tile can have (16 to 128, from R) by 128 B, of
+// which the smallest box that holds the tile's is copied.  Where even 128-column
+// tiles leave SMs idle, the CTAs of a cluster share a tile's K.
 //
-// What bounds it, on one B200 (6.56 TB/s copy rate): the weights' stream (E 128,
-// 2880 x 5760, 8192 rows in 344 us, 6.4 TB/s; E 64, 1536 x 4096, 256 rows in 54.6
-// us, of which 5 pass before the first copies have landed and 1.4 are the seventh
-// wave of 6.8; one token to 8 of those experts 12.8 us); with few tiles the chain
-// of stages in one SM, 0.27 us for 128 columns by 128 of K and 0.4 for 256; with a
-// short K the epilogue's latency, 1.2 us for a tile of 2 rows and K 64.
+// What bounds it, on one B200 (6.56 TB/s copy rate), the rows' quantiser included:
+// the weights' stream (E 64, 4096 x 3072, 256 rows in 124 us, 6.5 TB/s; 1536 x 4096
+// with 40 experts reached 53.3 us, of which about 3 are start-up and 1.4 the seventh
+// wave of 6.8; one token to 8 of those experts 12.5 us, 7.7 at the copy rate); with
+// few tiles the chain of stages in one SM, 0.15 us for each 128 of K (one row of K
+// 7168: 17.3 us by one SM, 9.6 by clusters of eight); with a short K the epilogue's
+// latency (E 135, K 64, 8848 columns, 2 rows per expert: 27.7 us, 0.9 a tile and SM).
 //
 // For gate_up a gate and its up column have to meet in one warp: interleaved
 // columns are neighbours, and concatenated ones are copied in groups of 8 gate

@@ -22,11 +22,10 @@
 // CTAs running together share a weight block through L2.
 //
 // What bounds it, on one B200: with a long K the 1000 W power limit (E 8, 4096 x
-// 28672, 8192 rows in 0.84 ms, 2.3 POP/s, at 1.38 GHz in a loop, 0.71 ms for a few
-// passes, 0.65 ms with all-zero weights at 1.965 GHz; pairs of CTAs with 256 x
+// 28672, 8192 rows in 0.80 to 0.85 ms, 2.3 POP/s, at 1.38 GHz in a loop, 0.65 ms with all-zero weights at 1.965 GHz; pairs of CTAs with 256 x
 // 256 tiles drew the same power for the same time), with a short one the
 // epilogue, whose shared-memory traffic fills 60% of its cycles (E 50, 240 x 2328,
-// 32200 rows in 66 us, 30 at the copy rate).
+// 32200 rows in 72 us with the quantiser, 30 at the copy rate).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -450,11 +449,11 @@ cudaError_t launch_gate_up(const Int8GemmArgs& a, cudaStream_t stream) {
 cudaError_t launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream) {
   if (a.R == 0) return cudaSuccess;
   // Few rows per expert go to the kernel with the operands exchanged
-  // (int8_few.cu): on one B200, 2 rows per expert (E 135, K 64, 8848 columns) 117 us
-  // here, 41 there; 24 rows (E 49, K 72) 76, 44; 64 rows (E 123, K 208) 222, 195; 96
-  // rows (E 128, K 2048) 78, 80; 127 rows (E 18, K 344) 38, 47.  So does what this
-  // one's 256-column tiles would leave half of the SMs idle with, in 128-column
-  // tiles (4 experts, 93 rows, K 6984: 36 us here, 37 there, 26 with 128 columns).
+  // (int8_few.cu): on one B200, 2 rows per expert (E 135, K 64, 8848 columns) 104 us
+  // here, 28 there; 24 rows (E 49, K 72) 18.8, 12.6; 64 rows (E 123, K 208) 107, 97;
+  // 80 rows (E 32, K 1024) 32.3, 32.4; 96 rows (E 128, K 2048) 70, 71; 128 rows (E 18,
+  // K 344) 21, 26.  So does what this one's 256-column tiles would leave half of the
+  // SMs idle with, in 128-column tiles (4 experts, 93 rows, K 6984: 39 us here, 22 there).
   const int64_t experts = std::min(a.E, a.R), columns = a.down ? a.H : 2 * static_cast<int64_t>(a.D);
   const int64_t tiles = (a.R / BM + experts) * ((columns + BN - 1) / BN);
   if (2 * tiles <= a.num_sms) return launch_int8_few(a, 128, stream);
