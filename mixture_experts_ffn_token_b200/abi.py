@@ -367,7 +367,7 @@ def moe_device_status(workspace, stream=None) -> int:
 _binding = None
 
 
-def _load_binding():
+def load_binding():
     """Load _binding.so (raises OSError when it has not been built)."""
     global _binding
     lib = load_library()
@@ -450,7 +450,7 @@ def moe_operator_workspace_size(cfg: MoEConfig) -> int:
 def moe_dispatch(cfg, x, inverse, rows, expert_weights=None, stream=None):
     """rows[inverse[t*k+j]] = expert_weights[t, j] * x[t]: tokens [T, H] (bf16
     or fp32) to rows sorted by expert [T*k, H]."""
-    st = (_binding or _load_binding()).dispatch(cfg, x, inverse, rows, expert_weights, stream)
+    st = (_binding or load_binding()).dispatch(cfg, x, inverse, rows, expert_weights, stream)
     if _done(st, "moe_dispatch"):
         return
     dt, dev = _rows_dtype("x", x), _device()
@@ -465,7 +465,7 @@ def moe_dispatch(cfg, x, inverse, rows, expert_weights=None, stream=None):
 def moe_dispatch_backward(cfg, d_rows, inverse, d_x, x=None, expert_weights=None, d_expert_weights=None, stream=None):
     """d_x[t] = sum_j expert_weights[t, j] * d_rows[inverse[t*k+j]] and, given x,
     d_expert_weights[t, j] = <x[t], d_rows[inverse[t*k+j]]>."""
-    st = (_binding or _load_binding()).dispatch_backward(cfg, d_rows, inverse, d_x, x, expert_weights,
+    st = (_binding or load_binding()).dispatch_backward(cfg, d_rows, inverse, d_x, x, expert_weights,
         d_expert_weights, stream)
     if _done(st, "moe_dispatch_backward"):
         return
@@ -484,7 +484,7 @@ def moe_dispatch_backward(cfg, d_rows, inverse, d_x, x=None, expert_weights=None
 
 def moe_combine(cfg, rows, inverse, out, expert_weights=None, stream=None):
     """out[t] = sum_j expert_weights[t, j] * rows[inverse[t*k+j]]."""
-    st = (_binding or _load_binding()).combine(cfg, rows, inverse, out, expert_weights, stream)
+    st = (_binding or load_binding()).combine(cfg, rows, inverse, out, expert_weights, stream)
     if _done(st, "moe_combine"):
         return
     dt, dev = _rows_dtype("rows", rows), _device()
@@ -501,7 +501,7 @@ def moe_combine_backward(cfg, d_out, inverse, d_rows, rows=None, expert_weights=
                          stream=None):
     """d_rows[inverse[t*k+j]] = expert_weights[t, j] * d_out[t] and, given rows,
     d_expert_weights[t, j] = <d_out[t], rows[inverse[t*k+j]]>."""
-    st = (_binding or _load_binding()).combine_backward(cfg, d_out, inverse, d_rows, rows, expert_weights,
+    st = (_binding or load_binding()).combine_backward(cfg, d_out, inverse, d_rows, rows, expert_weights,
         d_expert_weights, stream)
     if _done(st, "moe_combine_backward"):
         return
@@ -523,7 +523,7 @@ def moe_route_backward(cfg, logits, expert_indices, d_expert_weights, d_logits, 
     """d_logits [T, logits_row_stride] (and d_global_scale [1], which needs a
     workspace of moe_operator_workspace_size) from the gradients of the
     weights that moe_route returned for expert_indices."""
-    st = (_binding or _load_binding()).route_backward(cfg, logits, expert_indices, d_expert_weights, d_logits,
+    st = (_binding or load_binding()).route_backward(cfg, logits, expert_indices, d_expert_weights, d_logits,
         d_sink_weights, global_scale, d_global_scale, workspace, stream)
     if _done(st, "moe_route_backward"):
         return
@@ -546,7 +546,7 @@ def moe_route_backward(cfg, logits, expert_indices, d_expert_weights, d_logits, 
 
 def moe_dispatch_int8(cfg, x, inverse, rows_q, row_scales, stream=None):
     """moe_dispatch of bf16 tokens to 8-bit rows [T*k, int8_pitch(H)] and their scales [T*k]."""
-    st = (_binding or _load_binding()).dispatch_int8(cfg, x, inverse, rows_q, row_scales, stream)
+    st = (_binding or load_binding()).dispatch_int8(cfg, x, inverse, rows_q, row_scales, stream)
     if _done(st, "moe_dispatch_int8"):
         return
     dev = _device()
@@ -561,7 +561,7 @@ def moe_dispatch_int8(cfg, x, inverse, rows_q, row_scales, stream=None):
 def moe_quantize_rows(cfg, h, expert_offsets, rows_q, row_scales, stream=None):
     """Activations h [T*k, D] bf16 to 8-bit rows [T*k, int8_pitch(D)] and their
     scales, up to row expert_offsets[E] (None: all)."""
-    st = (_binding or _load_binding()).quantize_rows(cfg, h, expert_offsets, rows_q, row_scales, stream)
+    st = (_binding or load_binding()).quantize_rows(cfg, h, expert_offsets, rows_q, row_scales, stream)
     if _done(st, "moe_quantize_rows"):
         return
     dev = _device()
@@ -596,7 +596,7 @@ def moe_grouped_linear_int8(cfg, contraction, rows_q, row_scales, w_q, w_scales,
                             bias=None, stream=None):
     """One contraction over rows sorted by expert, in 8-bit integers: "gate_up"
     with the activation to out [T*k, D], "down" to out [T*k, H] (bf16)."""
-    st = (_binding or _load_binding()).grouped_linear_int8(cfg, CONTRACTIONS.get(contraction), rows_q, row_scales, w_q,
+    st = (_binding or load_binding()).grouped_linear_int8(cfg, CONTRACTIONS.get(contraction), rows_q, row_scales, w_q,
         w_scales, expert_offsets, out, workspace, bias, stream)
     if _done(st, "moe_grouped_linear_int8"):
         return

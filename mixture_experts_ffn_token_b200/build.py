@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libmoe_b200.so")
 BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
-CUDA_HOME = os.path.dirname(os.path.dirname(NVCC))
+CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2"]
 
@@ -29,16 +29,14 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _inputs():
-    return sources() + [os.path.join(CSRC, "binding.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(os.path.dirname(HERE), "include", "moe.h"), __file__]
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    both = [os.path.join(os.path.dirname(HERE), "include", "moe.h"), __file__]
+    inputs = {LIB: sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + both, BINDING: [BINDING_SOURCE] + both}
+    return all(os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in paths)
+               for out, paths in inputs.items())
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -65,9 +63,9 @@ def build_binding():
     root = os.path.dirname(torch.__file__)
     include = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
                os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(CUDA_HOME, "include")]
-    tmp = BINDING + ".tmp"
+    tmp = f"{BINDING}.{os.getpid()}.tmp"
     subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-                    os.path.join(CSRC, "binding.cpp"), "-o", tmp, *(f"-I{d}" for d in include),
+                    BINDING_SOURCE, "-o", tmp, *(f"-I{d}" for d in include),
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-L" + os.path.join(root, "lib"),
                     "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
     os.replace(tmp, BINDING)
