@@ -64,7 +64,7 @@ def build_binding():
     include = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
                os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(CUDA_HOME, "include")]
     tmp = f"{BINDING}.{os.getpid()}.tmp"
-    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                     BINDING_SOURCE, "-o", tmp, *(f"-I{d}" for d in include),
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-L" + os.path.join(root, "lib"),
                     "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
