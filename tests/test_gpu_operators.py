@@ -837,6 +837,57 @@ def test_two_calls_at_once():
         assert torch.equal(j["h"], w) and abi.moe_device_status(j["ws"]) == 0
 
 
+def test_calls_from_threads():
+    """Four threads, a stream each, make the same kinds of calls at once."""
+    import threading
+    T, H, D, E, k = 40, 264, 136, 6, 2
+    cfg = abi.config(T, H, E, k, D)
+    g = torch.Generator().manual_seed(3)
+    w_q = torch.randint(-127, 128, (E, 2 * D, abi.int8_pitch(H)), generator=g, dtype=torch.int8).cuda()
+    w_s = (torch.rand(E, 2 * D, generator=g) * 0.01).cuda()
+    jobs = []
+    for i in range(4):
+        _, off, inv = R.routing(T, E, k, seed=60 + i, drop=0.1 * i)
+        jobs.append(dict(off=off.cuda(), inv=inv.cuda(), x=randn(60 + i, T, H, dtype=BF16).cuda(), stream=torch.cuda.Stream(),
+                         q=torch.zeros(T * k, abi.int8_pitch(H), dtype=torch.int8, device="cuda"),
+                         s=torch.zeros(T * k, device="cuda"), h=torch.zeros(T * k, D, dtype=BF16, device="cuda"),
+                         rows=torch.zeros(T * k, H, dtype=BF16, device="cuda"), out=torch.zeros(T, H, dtype=BF16, device="cuda"),
+                         ws=torch.empty(abi.moe_operator_workspace_size(cfg), dtype=torch.uint8, device="cuda")))
+
+    def run(j):
+        abi.moe_dispatch(cfg, j["x"], j["inv"], j["rows"])
+        abi.moe_combine(cfg, j["rows"], j["inv"], j["out"])
+        abi.moe_dispatch_int8(cfg, j["x"], j["inv"], j["q"], j["s"])
+        abi.moe_grouped_linear_int8(cfg, "gate_up", j["q"], j["s"], w_q, w_s, j["off"], j["h"], j["ws"])
+
+    want = []
+    for j in jobs:
+        run(j)
+        torch.cuda.synchronize()
+        want.append((j["out"].clone(), j["h"].clone()))
+        j["out"].zero_(), j["h"].zero_()
+    torch.cuda.synchronize()
+    errors = []
+
+    def thread(j):
+        try:
+            with torch.cuda.stream(j["stream"]):
+                for _ in range(50):
+                    run(j)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=thread, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for j, (out, h) in zip(jobs, want):
+        assert torch.equal(j["out"], out) and torch.equal(j["h"], h) and abi.moe_device_status(j["ws"]) == 0
+
+
 def test_int8_shared_k_captured_and_at_once():
     """A K shared by blocks, captured: two graphs (a workspace each) replayed on two
     streams at the same time, on inputs that change between the replays."""

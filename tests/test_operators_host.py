@@ -181,3 +181,16 @@ def test_reference_forms():
     # ties of the rounding go to the even value, and the largest to 127
     q, s = R.quantize(torch.tensor([[127.0, 0.5, 1.5, -63.5, -127.0, 2.5]], dtype=torch.bfloat16))
     assert q.tolist() == [[127, 0, 2, -64, -127, 2]] and float(s) == 1.0
+
+
+def test_missing_binding_is_reported(monkeypatch):
+    """Without _binding.so the operators say so; there is no other way in."""
+    import sys
+
+    import mixture_experts_ffn_token_b200 as pkg
+    monkeypatch.setattr(abi, "_binding", None)
+    monkeypatch.delattr(pkg, "_binding", raising=False)
+    monkeypatch.setitem(sys.modules, pkg.__name__ + "._binding", None)
+    x, inv = torch.zeros(3, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(OSError, match="_binding.so"):
+        abi.moe_dispatch(abi.config(3, 64, 2, 1, 8), x, inv, torch.zeros(3, 64, dtype=torch.bfloat16))
