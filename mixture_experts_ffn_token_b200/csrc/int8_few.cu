@@ -12,12 +12,13 @@
 // tiles leave SMs idle, the CTAs of a cluster share a tile's K.
 //
 // What bounds it, on one B200 (6.56 TB/s copy rate), the rows' quantiser included:
-// the weights' stream (E 64, 4096 x 3072, 256 rows in 124 us, 6.5 TB/s; 1536 x 4096
-// with 40 experts reached 53.3 us, of which about 3 are start-up and 1.4 the seventh
-// wave of 6.8; one token to 8 of those experts 12.5 us, 7.7 at the copy rate); with
-// few tiles the chain of stages in one SM, 0.15 us for each 128 of K (one row of K
-// 7168: 17.3 us by one SM, 9.6 by clusters of eight); with a short K the epilogue's
-// latency (E 135, K 64, 8848 columns, 2 rows per expert: 27.7 us, 0.9 a tile and SM).
+// the weights' stream (E 64, K 4096, 2 x 1536 columns, 256 rows in 124 us, 6.5
+// TB/s; K 1536, 4096 columns in 53.3 us, of which about 3 are start-up and 1.4 the
+// seventh wave of 6.8; one token to 8 of those experts 12.5 us, 7.7 at the copy
+// rate); with few tiles the chain of stages in one SM, 0.15 us for each 128 of K
+// (one row of K 7168: 17.3 us by one SM, 9.6 by clusters of eight); with a short K
+// the epilogue's latency (E 135, K 64, 8848 columns, 2 rows per expert: 27.7 us,
+// 0.9 a tile and SM).
 //
 // For gate_up a gate and its up column have to meet in one warp: interleaved
 // columns are neighbours, and concatenated ones are copied in groups of 8 gate
