@@ -228,9 +228,9 @@ struct RouterGradArgs {
   const float* d_sink;       // [T,S] or null for zero
   void* d_logits;            // [T,stride], columns 0 .. E+S-1 written
   double* partial;           // [kGradMaxBlocks] or null: no d_global_scale
+  float* d_global_scale;     // [1], with partial
 };
-cudaError_t launch_route_grad(const RouterGradArgs& a, bool sink, bool bf16, float* d_global_scale,
-                              cudaStream_t stream);
+cudaError_t launch_route_grad(const RouterGradArgs& a, bool sink, bool bf16, cudaStream_t stream);
 
 // ------------------------------------------------------------ 8-bit experts
 // Bytes of a row of n 8-bit values: TMA row strides are multiples of 16.

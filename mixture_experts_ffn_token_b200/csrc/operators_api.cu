@@ -191,8 +191,8 @@ moe_status_t moe_route_backward(const moe_config_t* cfg, const void* logits, con
   a.d_sink = d_sink_weights;
   a.d_logits = d_logits;
   a.partial = d_global_scale != nullptr ? at<double>(workspace, kHeaderBytes) : nullptr;
-  return cuda_status(
-      moe::launch_route_grad(a, sink, cfg->logits_dtype == MOE_DTYPE_BF16, d_global_scale, s));
+  a.d_global_scale = d_global_scale;
+  return cuda_status(moe::launch_route_grad(a, sink, cfg->logits_dtype == MOE_DTYPE_BF16, s));
 }
 
 moe_status_t moe_dispatch_int8(const moe_config_t* cfg, const void* x, const int32_t* inverse, int8_t* rows_q,

@@ -15,8 +15,9 @@
 // a token, so a warp works on 32 / W, and its rows are zeroed in 16-byte
 // stores while the entries' loads are in flight; the entries follow.  8192
 // tokens of 128 + 2 lanes take 3.6 us, 4.8 with the global scale's gradient (a
-// second launch that sums the blocks' parts in order); a warp per token that
-// built its row in shared memory took 8.0 and 9.4.
+// second launch that sums the blocks' parts in order; tokens of one block need
+// none, 16 of them 4.8 -> 3.0 us a call); a warp per token that built its row in
+// shared memory took 8.0 and 9.4.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -134,7 +135,9 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const Route
     if (threadIdx.x == 0) {
       double s = 0.0;
       for (int w = 0; w < kGradWarps; ++w) s += s_sum[w];
-      a.partial[blockIdx.x] = s;
+      // (one block's part is the sum: no second launch)
+      if (gridDim.x == 1) *a.d_global_scale = static_cast<float>(s * static_cast<double>(a.route_scale));
+      else a.partial[blockIdx.x] = s;
     }
   }
 }
@@ -179,14 +182,13 @@ cudaError_t launch_grad(const RouterGradArgs& a, int* blocks, cudaStream_t strea
 
 }  // namespace
 
-cudaError_t launch_route_grad(const RouterGradArgs& a, bool sink, bool bf16, float* d_global_scale,
-                              cudaStream_t stream) {
+cudaError_t launch_route_grad(const RouterGradArgs& a, bool sink, bool bf16, cudaStream_t stream) {
   int blocks = 0;
   const cudaError_t err = sink ? (bf16 ? launch_grad<true, true>(a, &blocks, stream) : launch_grad<true, false>(a, &blocks, stream))
                                : (bf16 ? launch_grad<false, true>(a, &blocks, stream) : launch_grad<false, false>(a, &blocks, stream));
-  if (err != cudaSuccess || a.partial == nullptr) return err;
+  if (err != cudaSuccess || a.partial == nullptr || blocks == 1) return err;
   return launch_pdl(scale_grad_kernel, dim3(1), dim3(kSumThreads), 0, stream, a.partial, blocks, a.route_scale,
-                    d_global_scale);
+                    a.d_global_scale);
 }
 
 }  // namespace moe
