@@ -226,6 +226,7 @@ moe_status_t moe_forward_timed(const moe_config_t* cfg, const void* x, const voi
  * of MOE_DEVICE_ERR_* since the last call that reset it), synchronizing
  * `stream`.  moe_forward resets the word in its first kernel;
  * moe_create_indices and moe_grouped_ffn reset it before their first kernel.
+ * (moe_grouped_linear_int8: see there.)
  * Returns MOE_ERR_DEVICE_TIMEOUT if a timeout bit is set, MOE_OK otherwise
  * (other bits are reported through *device_status only). */
 moe_status_t moe_device_status(const void* workspace, int32_t* device_status, moe_stream_t stream);
@@ -433,9 +434,13 @@ moe_status_t moe_quantize_weights(const moe_config_t* cfg, moe_contraction_t whi
  *   rows_q, w_q, w_scales, out, bias  16-byte aligned.
  *   bias       [E, N] bf16, per has_bias.
  *   out        bf16, rows at and behind expert_offsets[E] left as they were.
- *   workspace  moe_operator_workspace_size(); its status word is reset by the
- *              call and read with moe_device_status (MOE_DEVICE_ERR_CSR: the
- *              offsets are no CSR of at most R rows, nothing was written).
+ *   workspace  moe_operator_workspace_size(), holding anything.  Its status
+ *              word, read with moe_device_status (MOE_DEVICE_ERR_CSR: the
+ *              offsets are no CSR of at most R rows, nothing was written), is
+ *              for the two calls of a layer: GATE_UP resets it, DOWN keeps what
+ *              the GATE_UP call before it on this workspace recorded, or resets
+ *              it if there was none since the last DOWN.  So read it after each
+ *              layer, or give each layer a workspace.
  * Numerics: exact 32-bit integer sums, scales, bias and activation in fp32,
  * one rounding to bf16; deterministic. */
 moe_status_t moe_grouped_linear_int8(const moe_config_t* cfg, moe_contraction_t which, const int8_t* rows_q,

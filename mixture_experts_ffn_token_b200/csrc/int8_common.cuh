@@ -66,6 +66,24 @@ struct Int8Params {
   int err_bit;
 };
 
+// The workspace's first two words: the device status, and a mark that gate_up
+// leaves and down takes away.  A layer runs both on one workspace and reads the
+// status once, after both: so gate_up starts the word anew, and down keeps what
+// the gate_up before it recorded, which only the mark tells from what the memory
+// held (a lone down starts the word anew; what gate_up cannot have recorded is
+// not its).  `bad_csr` is what this call found so far; a wait that times out is
+// recorded seconds later.  One thread of the last epilogue warp has read the
+// words (csr_pieces) and writes them once its first loads are on their way: by
+// thread 0 ahead of the barrier it cost one token 0.2 to 0.5 us.
+constexpr int kGateUpMark = 0x6d6f6547;
+__device__ __forceinline__ bool keeps_status() { return blockIdx.x == 0 && threadIdx.x == blockDim.x - 1; }
+__device__ __forceinline__ void start_status(int* status, const int2& before, bool down, bool bad_csr) {
+  constexpr int kOfGateUp = MOE_DEVICE_ERR_CSR | MOE_DEVICE_ERR_TIMEOUT_GEMM1;
+  const bool keep = down && before.y == kGateUpMark && (before.x & ~kOfGateUp) == 0;
+  status[0] = (keep ? before.x : 0) | (bad_csr ? MOE_DEVICE_ERR_CSR : 0);
+  status[1] = down ? 0 : kGateUpMark;
+}
+
 // The gated activation with sigmoids throughout (0.5 (1 + tanh a) is
 // sigmoid(2a)): exp2 and reciprocal approximations of about 2^-22, below the
 // bf16 rounding of h.  For large negative gates the exponential overflows and
@@ -164,15 +182,16 @@ __device__ __forceinline__ TileCoord warp_tile(int t, int from, int n_tiles, int
 }
 
 // Reads and checks the offsets and builds s_mt; returns the number of pieces, 0
-// for offsets that are no CSR (recorded in *status).  While the kernels before
+// for offsets that are no CSR (*bad_flag).  While the kernels before
 // (as a rule the rows' quantiser) still run, `prefetch` is called by warp 0 to
 // fetch the first tile's weights to L2, where their copies then find them: a
 // hint, which cannot make a value stale.  The offsets that it goes by may still
 // be changing, so it gets any CSR, and they are read again afterwards.  On return
-// the kernels before are complete and visible.
+// the kernels before are complete and visible, and `before` holds the status
+// words for the thread that keeps them.
 template <typename Prefetch>
 __device__ __forceinline__ int csr_pieces(const Int8Params& g, int* s_off, int* s_mt, int* bad_flag, int piece,
-                                          Prefetch prefetch) {
+                                          int2& before, Prefetch prefetch) {
   const int lane = threadIdx.x & 31;
   auto read = [&]() {
     for (int i = threadIdx.x; i <= g.E; i += blockDim.x) s_off[i] = __ldcg(g.offsets + i);
@@ -186,9 +205,7 @@ __device__ __forceinline__ int csr_pieces(const Int8Params& g, int* s_off, int* 
     if (*bad_flag == 0) prefetch();
   }
   griddep_wait();
-  // the status word of this call starts at zero: only this CTA records a bad
-  // CSR, and a timed-out wait of another comes seconds later
-  if (blockIdx.x == 0 && threadIdx.x == 0) *g.status = 0;
+  before = keeps_status() ? __ldcg(reinterpret_cast<const int2*>(g.status)) : make_int2(0, 0);
   bool same = true;
   for (int i = threadIdx.x; i <= g.E; i += blockDim.x) same = same && s_off[i] == __ldcg(g.offsets + i);
   if (!__syncthreads_and(same)) {
@@ -198,9 +215,7 @@ __device__ __forceinline__ int csr_pieces(const Int8Params& g, int* s_off, int* 
     if (threadIdx.x < 32) build_pieces(s_off, s_mt, bad_flag, g.E, g.R, piece, lane);
     __syncthreads();
   }
-  const bool bad = *bad_flag != 0;
-  if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(g.status, MOE_DEVICE_ERR_CSR);
-  return bad ? 0 : s_mt[g.E];
+  return *bad_flag != 0 ? 0 : s_mt[g.E];
 }
 
 }  // namespace moe

@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
-  const int pieces = csr_pieces(p.g, s_off, s_mt, bad_flag, BR, [&]() {
+  int2 before;
+  const int pieces = csr_pieces(p.g, s_off, s_mt, bad_flag, BR, before, [&]() {
     if (first >= s_mt[p.g.E] * p.g.n_tiles) return;
     const TileCoord tc = warp_tile(first, 0, p.g.n_tiles, p.g.E, s_mt, s_off, BR);
     for (int kb = kb0 + lane; kb < min(kb1, kb0 + p.ahead); kb += 32) {
@@ -332,6 +333,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     };
     Ahead next = {};
     if (first < total) next = fetch(first, 0);
+    if (keeps_status()) start_status(p.g.status, before, MODE == MODE_DOWN, *bad_flag != 0);
     if constexpr (SPLIT) {
       const TileCoord tc = next.tc;
 #pragma unroll

@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
-  const int pieces = csr_pieces(p, s_off, s_mt, bad_flag, BM, [&]() {
+  int2 before;
+  const int pieces = csr_pieces(p, s_off, s_mt, bad_flag, BM, before, [&]() {
     const int t = blockIdx.x;
     if (t >= s_mt[p.E] * p.n_tiles) return;
     const TileCoord tc = decode_tile(t, p.n_tiles, p.E, s_mt, s_off, BM);
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint8_t* stage = s_stage + (warp - 2) * kWarpStage;
     Ahead next = {};
     if (static_cast<int>(blockIdx.x) < total) next = fetch<MODE>(p, blockIdx.x, 0, s_mt, s_off, quad, part, lane);
+    if (keeps_status()) start_status(p.status, before, MODE == MODE_DOWN, *bad_flag != 0);
     int ti = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++ti) {
       const int acc = ti & 1;

@@ -12,8 +12,8 @@ using moe::validate_config;
 
 namespace {
 
-// The operators' workspace: the header (device status word), then one double
-// per block of the router gradient.
+// The operators' workspace: the header (device status word, and the 8-bit
+// products' mark beside it), then one double per block of the router gradient.
 constexpr size_t kHeaderBytes = 256;
 constexpr size_t kOperatorWorkspace = kHeaderBytes + moe::kGradMaxBlocks * sizeof(double);
 
