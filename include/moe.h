@@ -440,7 +440,8 @@ moe_status_t moe_quantize_weights(const moe_config_t* cfg, moe_contraction_t whi
  *              for the two calls of a layer: GATE_UP resets it, DOWN keeps what
  *              the GATE_UP call before it on this workspace recorded, or resets
  *              it if there was none since the last DOWN.  So read it after each
- *              layer, or give each layer a workspace.
+ *              layer, or give each layer a workspace.  A call of no tokens
+ *              does this too; it may also come without a workspace.
  * Numerics: exact 32-bit integer sums, scales, bias and activation in fp32,
  * one rounding to bf16; deterministic. */
 moe_status_t moe_grouped_linear_int8(const moe_config_t* cfg, moe_contraction_t which, const int8_t* rows_q,

@@ -439,6 +439,13 @@ cudaError_t launch_mode(const Int8GemmArgs& a, cudaStream_t stream) {
   return launch_pdl(int8_gemm_kernel<MODE, ACT>, grid, dim3(NUM_THREADS), smem_bytes(a.E), stream, mapA, mapAh, mapB, p);
 }
 
+// A call of no tokens: only the status words are written.
+__global__ void int8_status_kernel(int* status, int down) {
+  griddep_wait();  // the previous kernel's results are complete and visible
+  griddep_launch_dependents();
+  start_status(status, *reinterpret_cast<const int2*>(status), down != 0, false);
+}
+
 template <int MODE>
 cudaError_t launch_gate_up(const Int8GemmArgs& a, cudaStream_t stream) {
   if (a.activation == MOE_ACT_SILU) return launch_mode<MODE, MOE_ACT_SILU>(a, stream);
@@ -449,7 +456,7 @@ cudaError_t launch_gate_up(const Int8GemmArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream) {
-  if (a.R == 0) return cudaSuccess;
+  if (a.R == 0) return launch_pdl(int8_status_kernel, dim3(1), dim3(1), 0, stream, a.status, a.down);
   // Few rows per expert go to the kernel with the operands exchanged
   // (int8_few.cu): on one B200, 2 rows per expert (E 135, K 64, 8848 columns) 104 us
   // here, 28 there; 24 rows (E 49, K 72) 18.8, 12.6; 64 rows (E 123, K 208) 107, 97;

@@ -31,6 +31,17 @@ moe_status_t check_rows(const moe_config_t* cfg, moe_dtype_t dtype, const int32_
   return MOE_OK;
 }
 
+// Whether p is memory of the current device, without touching it.
+bool device_memory(const void* p) {
+  int dev = 0;
+  cudaPointerAttributes attr;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return (attr.type == cudaMemoryTypeDevice && attr.device == dev) || attr.type == cudaMemoryTypeManaged;
+}
+
 bool given(const void* p) { return p != nullptr && aligned16(p); }
 bool given_or_null(const void* p) { return aligned16(p); }
 
@@ -250,7 +261,15 @@ moe_status_t moe_grouped_linear_int8(const moe_config_t* cfg, moe_contraction_t 
   const NvtxRange api_range("moe_grouped_linear_int8");
   moe_status_t st = check_int8(cfg, which);
   if (st != MOE_OK) return st;
-  if (cfg->num_tokens == 0) return MOE_OK;
+  if (cfg->num_tokens == 0) {
+    // nothing but the status, where there is a word for it: such a call may
+    // come without pointers, as the other entry points take it
+    if (check_operator_workspace(workspace, workspace_bytes) != MOE_OK || !device_memory(workspace)) return MOE_OK;
+    moe::Int8GemmArgs a = {};
+    a.down = which == MOE_DOWN ? 1 : 0;
+    a.status = at<int>(workspace, 0);
+    return cuda_status(moe::launch_int8_gemm(a, reinterpret_cast<cudaStream_t>(stream)));
+  }
   if (!given(rows_q) || row_scales == nullptr || !given(w_q) || !given(w_scales) || expert_offsets == nullptr ||
       !given(out))
     return MOE_ERR_INVALID_ARGUMENT;

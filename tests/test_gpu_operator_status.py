@@ -99,3 +99,41 @@ def test_status_of_a_captured_layer():
         p.bad.copy_(offsets)
         graph.replay()
         assert p.status() == want
+
+
+@pytest.mark.parametrize("part", ["gate_up", "down"])
+@pytest.mark.parametrize("captured", [False, True])
+def test_status_of_no_tokens(part, captured):
+    """A batch of no tokens is a success: its status is not what the memory held before."""
+    for fill in (255, 2, 0):
+        p = Products(0, fill=fill)
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                p.run(part)
+            graph.replay()
+        else:
+            p.run(part)
+        assert p.status() == 0
+
+
+def test_no_tokens_follow_the_same_rule():
+    full, empty = Products(300), Products(0)
+    full.run("gate_up", bad=True)
+    empty.run("down", workspace=full.workspace)        # keeps what gate_up recorded
+    assert full.status() == CSR
+    empty.run("gate_up", workspace=full.workspace)     # starts anew
+    assert full.status() == 0
+    full.run("gate_up")
+    full.record(GEMM1)
+    empty.run("gate_up", workspace=full.workspace)
+    full.run("down")
+    assert full.status() == 0
+
+
+def test_no_tokens_without_a_workspace():
+    """From C, a batch of no tokens needs no pointer."""
+    cfg = abi.config(0, 64, 3, 1, 72)
+    fn = abi.load_library().moe_grouped_linear_int8
+    for which in (0, 1):
+        assert fn(ctypes.byref(cfg), which, None, None, None, None, None, None, None, None, 0, None) == 0
