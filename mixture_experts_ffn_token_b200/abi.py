@@ -368,14 +368,19 @@ _binding = None
 
 
 def load_binding():
-    """Load _binding.so (raises OSError when it has not been built)."""
+    """Load _binding.so (raises OSError when it has not been built, or was built
+    for another torch or Python)."""
     global _binding
+    from .build import binding_target
     lib = load_library()
     try:
         from . import _binding as b
     except ImportError as e:
         raise OSError(f"_binding.so cannot be loaded ({e}): build it with "
                       "`python -m mixture_experts_ffn_token_b200.build`") from e
+    if getattr(b, "target", None) != binding_target():
+        raise OSError(f"_binding.so is for {getattr(b, 'target', 'another torch')}, this is {binding_target()}: build it "
+                      "with `python -m mixture_experts_ffn_token_b200.build`")
     b.use(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
         "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward", "moe_route_backward",
         "moe_dispatch_int8", "moe_quantize_rows", "moe_grouped_linear_int8")))

@@ -340,4 +340,13 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&kModule); }
+// `target`: the torch and Python whose objects this file reads; load_binding()
+// refuses to use it under others.
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m != nullptr && PyModule_AddStringConstant(m, "target", MOE_BINDING_TARGET) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
