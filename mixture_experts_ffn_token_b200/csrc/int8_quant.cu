@@ -4,10 +4,12 @@
 // within half a step.
 //
 // The rounding is exact although it is one multiply by a rounded reciprocal:
-// a and m have 8-bit significands, so 127 a / m is either a tie or at least
-// 2^-9 away from one, far beyond the reciprocal's error; the ties are a = m/2
-// (63.5, to 64) and those of an m whose reciprocal times 127 is a power of two
-// (exact).  The reciprocal is rounded up, so 63.5 never falls below its tie.
+// with 8-bit significands A and M, a / m = A / (M 2^s), a quotient 127 a / m that
+// is no tie lies at least 1 / (2 M 2^s) from one, and the reciprocal's error
+// moves it by less than 2^-23 of itself, 127 A 2^-23 / (M 2^s), which is under
+// 1/128 of that.  The ties are a = m/2 (63.5, to 64) and those of an m whose
+// reciprocal times 127 is a power of two (exact).  The reciprocal is rounded up,
+// so 63.5 never falls below its tie.
 // Bound by HBM: each value read once and each place written once.
 // Rows of denormal size are scaled by 2^64 first.  A row that holds an
 // infinity or a NaN gets a NaN scale, so that its products are NaN.
