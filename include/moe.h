@@ -442,8 +442,9 @@ moe_status_t moe_quantize_weights(const moe_config_t* cfg, moe_contraction_t whi
  *              it if there was none since the last DOWN.  So read it after each
  *              layer, or give each layer a workspace.  A call of no tokens
  *              does this too; it may also come without a workspace.
- * Numerics: exact 32-bit integer sums, scales, bias and activation in fp32,
- * one rounding to bf16; deterministic. */
+ * Numerics: exact 32-bit integer sums; their conversion, the scales and the
+ * bias in fp32, the activation with an exponential of 2 + 1.17 |x| steps of
+ * 2^-23, and last the rounding to bf16; deterministic. */
 moe_status_t moe_grouped_linear_int8(const moe_config_t* cfg, moe_contraction_t which, const int8_t* rows_q,
                                      const float* row_scales, const int8_t* w_q, const float* w_scales,
                                      const void* bias, const int32_t* expert_offsets, void* out, void* workspace,

@@ -85,8 +85,10 @@ __device__ __forceinline__ void start_status(int* status, const int2& before, bo
 }
 
 // The gated activation with sigmoids throughout (0.5 (1 + tanh a) is
-// sigmoid(2a)): exp2 and reciprocal approximations of about 2^-22, below the
-// bf16 rounding of h.  For large negative gates the exponential overflows and
+// sigmoid(2a)).  The exponential's error grows with its argument, 2 + 1.17 |x|
+// steps of 2^-23: 2^-22 near zero, 2^-18 at -20, 2^-16 at -87, where the
+// sigmoid ends, and so it stays below the bf16 rounding of h, 2^-8.  The
+// quotient's is 2 steps.  For large negative gates the exponential overflows and
 // the quotient is 0, as the limit is.  ACT is a template argument: a branch per
 // element would keep the elements from overlapping.
 template <int ACT>

@@ -3,9 +3,9 @@
 // for p in expert e's segment; the gate_up product also applies the gated
 // activation and stores h [R, D], the down product stores [R, H].
 //
-// The integer sums are exact (32-bit accumulators in TMEM, K <= 131072), the
-// scales, bias and activation are fp32, and the only rounding is the store to
-// bf16.  Both operands are K-major (the weights are turned once, when they are
+// The integer sums are exact (32-bit accumulators in TMEM, K <= 131072).  The
+// sum's conversion to fp32, the two scales and the bias round to 2^-24 each, the
+// activation as int8_common.cuh says, and the store to bf16 to 2^-8.  Both operands are K-major (the weights are turned once, when they are
 // quantised), so a 128-byte swizzle row holds 128 values of K: a stage of
 // 48 KB carries twice the K of the bf16 kernel's, and streaming the weights
 // costs half the bytes.
