@@ -410,7 +410,9 @@ typedef enum { MOE_GATE_UP = 0, MOE_DOWN = 1 } moe_contraction_t;
 /* moe_dispatch of x [T, H] bf16 to 8-bit rows: every token is quantised once
  * and written to its slots' positions.
  *   rows_q      [R, MOE_INT8_PITCH(H)] out, row_scales [R] fp32 out; rows of
- *               no slot are left as they were. */
+ *               no slot are left as they were.
+ * It takes no routing weights: to weight the experts' inputs, multiply
+ * row_scales[p] by the slot's weight before the product. */
 moe_status_t moe_dispatch_int8(const moe_config_t* cfg, const void* x, const int32_t* inverse, int8_t* rows_q,
                                float* row_scales, moe_stream_t stream);
 
